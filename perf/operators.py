@@ -245,7 +245,8 @@ def _plain_plan(s):
     pos = ctx[seq] + row - cu[seq]
     slot = table[seq, (pos // page).clamp(0, width - 1)].long() * page + pos % page
     return (torch.where(live, slot, -1).int(), torch.where(live, pos, -1).int(),
-            torch.where(served, ctx + new, ctx).int(), (avail - taken).int(), (~served).sum().int().view(1), table, free)
+            torch.where(served, ctx + new, ctx).int(),
+            torch.where(served, ctx + new, s["held"].long()).int(), (avail - taken).int(), (~served).sum().int().view(1), table, free)
 
 
 def _plain_write(s):
