@@ -1,4 +1,4 @@
-"""MI355X (gfx950) RG-LRU and gated delta rule: HIP kernels behind a C ABI (include/*.h) and this thin binding."""
+"""MI355X (gfx950) RG-LRU, gated delta rule and paged attention: HIP kernels behind a C ABI (include/*.h) and this thin binding."""
 from . import _lib
 from ._lib import RglruError, header_symbols  # noqa: F401
 from .ops import (  # noqa: F401
@@ -18,6 +18,10 @@ from .ops import (  # noqa: F401
     rglru_delta_ckpt_elems,
     rglru_delta_rule_bwd,
     rglru_delta_rule_fwd,
+    rglru_page_plan,
+    rglru_paged_attn_fwd,
+    rglru_paged_attn_workspace_bytes,
+    rglru_paged_kv_write,
     rglru_ckpt_elems,
     rglru_fwd,
     rglru_fwd_scratch,

@@ -53,6 +53,25 @@ class rglru_delta_shape_t(ctypes.Structure):
     ]
 
 
+class rglru_paged_shape_t(ctypes.Structure):
+    _fields_ = [
+        ("n_tokens", c_int64),
+        ("n_pages", c_int64),
+        ("n_seqs", c_int32),
+        ("max_pages", c_int32),
+        ("page_size", c_int32),
+        ("q_heads", c_int32),
+        ("kv_heads", c_int32),
+        ("head_dim", c_int32),
+        ("io_dtype", c_int32),
+        ("max_new", c_int32),
+        ("window", c_int32),
+        ("scale", c_float),
+        ("q_stride", c_int64),
+        ("kv_stride", c_int64),
+    ]
+
+
 _vp = c_void_p
 _SIGNATURES = {
     "rglru_ckpt_elems": (c_size_t, [POINTER(rglru_shape_t)]),
@@ -82,6 +101,10 @@ _SIGNATURES = {
     "rglru_delta_rule_bwd": (c_int, [POINTER(rglru_delta_shape_t), _vp, c_int64] + [_vp] * 15 + [c_size_t, _vp]),
     "rglru_delta_chunk_workspace_bytes": (c_size_t, [POINTER(rglru_delta_shape_t), c_int64]),
     "rglru_delta_chunk_fwd": (c_int, [POINTER(rglru_delta_shape_t), _vp, c_int64] + [_vp] * 9 + [c_size_t, _vp]),
+    "rglru_page_plan": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 13),
+    "rglru_paged_kv_write": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 6),
+    "rglru_paged_attn_workspace_bytes": (c_size_t, [POINTER(rglru_paged_shape_t)]),
+    "rglru_paged_attn_fwd": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 9 + [c_size_t, _vp]),
     "rglru_status_string": (ctypes.c_char_p, [c_int]),
     "rglru_abi_version": (c_int, []),
 }

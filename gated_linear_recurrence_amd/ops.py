@@ -600,3 +600,164 @@ def rglru_delta_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
                                    _ptr(workspace), workspace.numel(), _stream(q.device))
     _lib.check(st, "rglru_delta_chunk_fwd")
     return o, final_state
+
+
+def _paged_cache(k_cache, v_cache, device):
+    """Checks a page cache pair; returns its shape [n_pages, Hkv, page_size, D]."""
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a tensor [n_pages, Hkv, page_size, D]")
+    if k_cache.dtype not in _IO:
+        raise ValueError(f"unsupported dtype {k_cache.dtype}")
+    _need(k_cache, "k_cache", k_cache.shape, k_cache.dtype, device)
+    _need(v_cache, "v_cache", k_cache.shape, k_cache.dtype, device)
+    return k_cache.shape
+
+
+def _rows(t, name, heads, dim, dtype, device):
+    """Checks packed rows [T, heads, dim], each row dense; returns (T, elements from one row to the next)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (T, {heads}, {dim})")
+    row, head, one = t.stride()
+    dense = heads * dim
+    if (one != 1 and dim > 1) or (head != dim and heads > 1):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if t.shape[0] < 2:
+        row = dense
+    if row < dense:
+        raise ValueError(f"the rows of {name} overlap")
+    return t.shape[0], row
+
+
+def _packed(cu_seqlens, device):
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [N + 1]")
+    n = cu_seqlens.numel() - 1
+    _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, device)
+    return n
+
+
+def _table(block_table, n, device):
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [N, max_pages]")
+    _need(block_table, "block_table", (n, block_table.shape[1]), torch.int32, device)
+    return block_table.shape[1]
+
+
+def _out(t, name, shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else _need(t, name, shape, dtype, device)
+
+
+def rglru_page_plan(context_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, *, n_tokens: int, page_size: int,
+                    held_lens: Optional[torch.Tensor] = None, max_new: int = 0,
+                    slot_map: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                    kv_lens: Optional[torch.Tensor] = None, held_lens_out: Optional[torch.Tensor] = None,
+                    free_count_out: Optional[torch.Tensor] = None, unserved: Optional[torch.Tensor] = None):
+    """Block table and slot map of a step, built on the GPU from the request lengths (all int32).
+
+    context_lens [N]: tokens in the cache; held_lens [N] (default: context_lens): tokens the table's pages were
+    taken for; cu_seqlens [N + 1]: the new tokens, packed; n_tokens: rows of the packed batch (those from
+    cu_seqlens[N] on are padding). block_table [N, max_pages] and free_pages [n_pages] (a stack of free_count [1]
+    entries) are updated in place: pages past a sequence's new length go back to the stack, then new ones are
+    popped in the order of sequences. max_new: the most new tokens of a sequence, 0 if not known.
+    Returns (slot_map [T], positions [T], kv_lens [N], held_lens_out [N], free_count_out [1], unserved [1]); a
+    sequence for which no pages are left is counted in unserved, its slots are -1, its lengths and pages stay."""
+    lib = _lib.load()
+    dev = context_lens.device
+    n = _packed(cu_seqlens, dev)
+    _need(context_lens, "context_lens", (n,), torch.int32, dev)
+    _opt(held_lens, "held_lens", (n,), torch.int32, dev)
+    width = _table(block_table, n, dev)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a tensor [n_pages]")
+    n_pages = free_pages.numel()
+    _need(free_pages, "free_pages", (n_pages,), torch.int32, dev)
+    _need(free_count, "free_count", (1,), torch.int32, dev)
+    t = int(n_tokens)
+    slot_map = _out(slot_map, "slot_map", (t,), torch.int32, dev)
+    positions = _out(positions, "positions", (t,), torch.int32, dev)
+    kv_lens = _out(kv_lens, "kv_lens", (n,), torch.int32, dev)
+    held_lens_out = _out(held_lens_out, "held_lens_out", (n,), torch.int32, dev)
+    free_count_out = _out(free_count_out, "free_count_out", (1,), torch.int32, dev)
+    unserved = _out(unserved, "unserved", (1,), torch.int32, dev)
+    shape = _lib.rglru_paged_shape_t(t, n_pages, n, width, int(page_size), 0, 0, 0, 0, int(max_new), 0, 0.0, 0, 0)
+    with torch.cuda.device(dev):
+        st = lib.rglru_page_plan(ctypes.byref(shape), _ptr(context_lens), _ptr(held_lens), _ptr(cu_seqlens),
+                                 _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
+                                 _ptr(slot_map), _ptr(positions), _ptr(kv_lens), _ptr(held_lens_out), _ptr(unserved),
+                                 _stream(dev))
+    _lib.check(st, "rglru_page_plan")
+    return slot_map, positions, kv_lens, held_lens_out, free_count_out, unserved
+
+
+def rglru_paged_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         slot_map: torch.Tensor) -> None:
+    """Writes rows of k and v [T, Hkv, D] into the slots slot_map [T] (int32; negative: skipped) of the caches.
+
+    Caches are [n_pages, Hkv, page_size, D], float32 or bfloat16 like k and v. The rows of k and v may be
+    slices of wider rows (one stride for both)."""
+    lib = _lib.load()
+    dev = k_cache.device
+    n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)
+    t, row = _rows(k, "k", heads, dim, k_cache.dtype, dev)
+    tv, row_v = _rows(v, "v", heads, dim, k_cache.dtype, dev)
+    if tv != t or row_v != row:
+        raise ValueError("k and v must have the same rows")
+    _need(slot_map, "slot_map", (t,), torch.int32, dev)
+    shape = _lib.rglru_paged_shape_t(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[k_cache.dtype], 0, 0, 0.0, 0, row)
+    with torch.cuda.device(dev):
+        st = lib.rglru_paged_kv_write(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
+                                      _ptr(slot_map), _stream(dev))
+    _lib.check(st, "rglru_paged_kv_write")
+
+
+def rglru_paged_attn_workspace_bytes(shape: _lib.rglru_paged_shape_t) -> int:
+    return int(_lib.load().rglru_paged_attn_workspace_bytes(ctypes.byref(shape)))
+
+
+def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                         cu_seqlens: torch.Tensor, kv_lens: torch.Tensor, *, max_new: int = 0, window: int = 0,
+                         scale: Optional[float] = None, want_lse: bool = True, o: Optional[torch.Tensor] = None,
+                         lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Causal attention of packed new tokens over a paged cache that holds their own keys and values already.
+
+    q [T, Hq, D] (rows may be slices of wider rows), caches [n_pages, Hkv, page_size, D], D 64, 128 or 256,
+    bfloat16 or float32; block_table [N, max_pages], cu_seqlens [N + 1] and kv_lens [N] (new tokens included)
+    int32. Row i of a sequence stands at kv_len - new + i and sees the keys up to its own, with window > 0 the
+    last `window` of them. max_new: the most new tokens of a sequence (0: not known; 1 for a decode step picks the
+    kernel for few rows). scale defaults to 1 / sqrt(D). workspace: a uint8 device tensor of at least
+    rglru_paged_attn_workspace_bytes bytes, 256-byte aligned (allocated here when None); calls sharing one must
+    not overlap. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
+    lib = _lib.load()
+    dev = k_cache.device
+    n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T, Hq, D]")
+    hq = q.shape[1]
+    t, row = _rows(q, "q", hq, dim, k_cache.dtype, dev)
+    n = _packed(cu_seqlens, dev)
+    _need(kv_lens, "kv_lens", (n,), torch.int32, dev)
+    width = _table(block_table, n, dev)
+    o = _out(o, "o", (t, hq, dim), q.dtype, dev)
+    if want_lse or lse is not None:
+        lse = _out(lse, "lse", (t, hq), torch.float32, dev)
+    sc = (1.0 / float(dim) ** 0.5) if scale is None else float(scale)
+    shape = _lib.rglru_paged_shape_t(t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], int(max_new),
+                                     int(window), sc, row, 0)
+    if workspace is None:
+        nbytes = int(lib.rglru_paged_attn_workspace_bytes(ctypes.byref(shape)))
+        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    with torch.cuda.device(dev):
+        st = lib.rglru_paged_attn_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), _ptr(q),
+                                      _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(workspace),
+                                      workspace.numel(), _stream(dev))
+    _lib.check(st, "rglru_paged_attn_fwd")
+    return o, lse

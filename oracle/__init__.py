@@ -1,10 +1,12 @@
 """Float64 CPU oracles: the RG-LRU scan and its block-diagonal gate projection,
-and the gated delta rule (GDN/KDA).
+the gated delta rule (GDN/KDA), and the paged cache with its attention
+(oracle.paged).
 
 TEST INFRASTRUCTURE ONLY: imported by tests/, by the smoke check and by the
 benchmark's CPU-baseline leg. The HIP library and its binding never import,
 call or link anything here.
 """
+from . import paged  # noqa: F401
 from .delta import chunk_gdn, recurrent_delta_rule, recurrent_delta_rule_backward  # noqa: F401
 from .rglru import (  # noqa: F401
     C_DEFAULT,
