@@ -1,8 +1,31 @@
 // Attention of new tokens over a paged key/value cache (include/paged_attn.h).
 //
-// One wave per row (token, query head): 64 keys at a time, a key per lane for
-// the scores, a column of the values per lane for the output, with the running
-// maximum and sum of the softmax.
+// Mathematics. A row is one (token, query head); the rows of a key head are
+// (token, head of its group) pairs in that order, so a group's heads share the
+// keys and values that a workgroup reads. A wave holds 32 rows as the columns
+// of S^T = K Q^T (32x32 MFMA): a lane owns one row, so the running maximum and
+// sum of the softmax are per-lane scalars and the sum over keys needs no
+// exchange but one between the two half-waves for the maximum. The
+// accumulator layout of S^T (keys 4h..4h+3 and 8+4h..8+4h+3 of every 16 in
+// half-wave h) is the operand layout of O^T = V^T P^T up to the order of the
+// keys, and the sum over keys does not care for their order: the weights go
+// from one product into the next without leaving their registers, and V^T is
+// read out of row-major V with the transposing LDS read (4 keys of one column
+// per lane). Scores, maxima, sums and outputs are float32; bf16 weights are
+// rounded to bf16 where they enter the product (what the matrix cores take).
+// The output is rescaled only where the maximum grew by more than 2^8: the
+// weights stay below 2^8 then, which costs float32 and bf16 nothing, and most tiles skip
+// the rescale.
+//
+// float32 uses the float32 MFMA with the same lane layouts, eight 2-deep
+// products for one 16-deep one.
+//
+// What a row must not see must not reach it, infinities and NaN included:
+// scores are replaced where they are masked, but a weight of 0 times an
+// infinite value is NaN. Tiles that some row of the wave does not see in full
+// therefore look at their values first; where one is not finite, the product
+// runs on the values with those replaced by 0, and two further products of
+// 0/1 operands tell which (row, column) pairs see a +inf, a -inf or a NaN.
 #include <hip/hip_runtime.h>
 
 #include "paged_common.h"
@@ -12,77 +35,845 @@ namespace paged {
 
 namespace {
 
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+typedef __attribute__((address_space(4))) const int32_t const_i32;  // read through the scalar cache
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;  // growth of the maximum (log2) that the weights absorb without a rescale
+
+// An operand of a 32x32x16 product: 8 elements per lane (16 bytes of bf16, 32 of float32).
+template <typename E>
+struct Frag;
+template <>
+struct Frag<uint16_t> {
+  static constexpr int kWords = 4;
+  static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u, kTop = 0x80008000u;
+  u32x4 w;
+};
+template <>
+struct Frag<float> {
+  static constexpr int kWords = 8;
+  static constexpr uint32_t kExp = 0x7F800000u, kOne = 0x00800000u, kTop = 0x80000000u;
+  u32x8 w;
+};
+
+__device__ __forceinline__ f32x16 mma(const Frag<uint16_t>& a, const Frag<uint16_t>& b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a.w), __builtin_bit_cast(bf16x8, b.w), c, 0,
+                                                 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(const Frag<float>& a, const Frag<float>& b, f32x16 c) {
+  const f32x8 x = __builtin_bit_cast(f32x8, a.w), y = __builtin_bit_cast(f32x8, b.w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[j], y[j], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ Frag<uint16_t> pack(const float* p, uint16_t) {
+  Frag<uint16_t> f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.w[j] = f32x2_to_bf16x2(p[2 * j], p[2 * j + 1]);
+  return f;
+}
+__device__ __forceinline__ Frag<float> pack(const float* p, float) {
+  Frag<float> f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f.w[j] = __float_as_uint(p[j]);
+  return f;
+}
+
+// Splits an operand into its finite elements and 0/1 operands marking +inf or NaN, and -inf or NaN.
+__device__ __forceinline__ void split(const Frag<uint16_t>& f, Frag<uint16_t>& fin, Frag<uint16_t>& up,
+                                      Frag<uint16_t>& down) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t c = 0, u = 0, d = 0;
+#pragma unroll
+    for (int s = 0; s < 32; s += 16) {
+      const uint32_t x = (f.w[j] >> s) & 0xFFFFu;
+      const bool odd = (x & 0x7F80u) == 0x7F80u, nan = odd && (x & 0x7Fu) != 0;
+      c |= (odd ? 0u : x) << s;
+      u |= (odd && (nan || x == 0x7F80u) ? 0x3F80u : 0u) << s;
+      d |= (odd && (nan || x == 0xFF80u) ? 0x3F80u : 0u) << s;
+    }
+    fin.w[j] = c;
+    up.w[j] = u;
+    down.w[j] = d;
+  }
+}
+__device__ __forceinline__ void split(const Frag<float>& f, Frag<float>& fin, Frag<float>& up, Frag<float>& down) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t x = f.w[j];
+    const bool odd = (x & 0x7F800000u) == 0x7F800000u, nan = odd && (x & 0x7FFFFFu) != 0;
+    fin.w[j] = odd ? 0u : x;
+    up.w[j] = odd && (nan || x == 0x7F800000u) ? 0x3F800000u : 0u;
+    down.w[j] = odd && (nan || x == 0xFF800000u) ? 0x3F800000u : 0u;
+  }
+}
+
+__device__ __forceinline__ float half_max(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// A tile of kRows rows of the cache in LDS, in pieces of 16 bytes. The piece
+// at column c of row r lies at column c ^ swizzle(r), chosen so that the 16
+// lanes that one LDS cycle serves fall on different banks: keys are read 16
+// bytes per lane down a column of rows, values 4 rows x 64 bytes at a time
+// (bf16, transposing) or a row of floats per half-wave (float32). The
+// swizzles are linear over XOR, so what depends on the instruction and on the
+// lane separates.
+template <typename E, int D>
+struct Tile {
+  static constexpr int kRowBytes = D * int(sizeof(E));
+  static constexpr int kCols = kRowBytes / 16;          // pieces of a row
+  static constexpr int kLoadRows = 64 / kCols;          // rows that one load of a wave fetches
+  __device__ static constexpr int swz_k(int r) { return kCols == 8 ? (r >> 1) & 7 : r & 15; }
+  __device__ static constexpr int swz_v(int r) {
+    return sizeof(E) == 4 ? ((r >> 2) & 1) << 3 : kCols == 8 ? ((r >> 1) & 1) << 2 : (r & 3) << 2;
+  }
+};
+
 struct AttnArgs {
   const int32_t* cu;
   const int32_t* kv_lens;
   const int32_t* table;
-  const void* q;
-  const void* kc;
-  const void* vc;
-  void* o;
+  const uint8_t* q;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  uint8_t* o;
   float* lse;
+  int64_t* sched;   // wide calls: the row tiles (see sched_kernel)
+  int32_t* joins;   // [grid][4]: what the join after workgroup b merges
+  float* parts;     // [grid][2]: partial results of a workgroup's first and last unit
   int64_t T, q_stride;
-  int32_t n_pages, N, width, lps, Hq, Hkv, window;
-  float scale;
+  int32_t n_pages, N, width, lps, Hq, Hkv, group, window, grid, max_tiles;
+  float scale2;     // |scale| log2 e (1 for a scale of 0, whose queries are zeroed)
+  int32_t q_sign;   // sign of the scale: -1, 0, 1
 };
 
-__device__ __forceinline__ float load1(const float* p, int64_t i) { return p[i]; }
-__device__ __forceinline__ float load1(const uint16_t* p, int64_t i) { return bf16_bits_to_f32(p[i]); }
-__device__ __forceinline__ void store1(float* p, int64_t i, float f) { p[i] = f; }
-__device__ __forceinline__ void store1(uint16_t* p, int64_t i, float f) { p[i] = f32_to_bf16(f); }
+// One sequence's lengths, clamped so that whatever is stored every access stays in bounds.
+struct Seq {
+  int32_t start, fresh, kv;
+};
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int n) {
+  Seq s;
+  const int64_t c0 = min(max(int64_t(a.cu[n]), int64_t(0)), a.T);
+  const int64_t c1 = min(max(int64_t(a.cu[n + 1]), c0), a.T);
+  s.start = int32_t(c0);
+  s.fresh = int32_t(c1 - c0);
+  s.kv = int32_t(min(max(int64_t(a.kv_lens[n]), int64_t(0)), (int64_t(a.width) << a.lps)));
+  return s;
+}
+
+// Positions of rows r0 .. r1 (inclusive) of a sequence, -1 before its start, and the tiles of kv that they see.
+struct Span {
+  int32_t first, last;  // positions
+  int32_t lo, hi;       // tiles [lo, hi), at least one
+};
+template <int BN>
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int32_t r0, int32_t r1) {
+  Span x;
+  x.first = max(s.kv - s.fresh + r0 / a.group, -1);
+  x.last = max(s.kv - s.fresh + r1 / a.group, -1);
+  x.lo = a.window > 0 ? max(x.first - a.window + 1, 0) / BN : 0;
+  x.hi = max((x.last + BN) / BN, x.lo + 1);
+  return x;
+}
+
+// Loads rows kv0 + i * kLoadRows .. of a tile of keys or values straight into LDS; `i` counts the tile's loads. All rows
+// of a load are in one page: kLoadRows is at most 8, the smallest page.
+template <typename E, int D, bool kValues>
+__device__ __forceinline__ void load_rows(const AttnArgs& a, const uint8_t* cache, const_i32* row, int hk,
+                                          int32_t kv0, int32_t last_page, int i, uint32_t tile, int lane) {
+  using L = Tile<E, D>;
+  const int32_t j = kv0 + i * L::kLoadRows;
+  const int32_t page = min(max(row[min(j >> a.lps, last_page)], 0), a.n_pages - 1);
+  const int64_t at = ((int64_t(page) * a.Hkv + hk) << a.lps) + (j & ((1 << a.lps) - 1));
+  const uint8_t* base = cache + at * L::kRowBytes;
+  const int r = lane / L::kCols, c = lane % L::kCols;
+  const int lane_swz = kValues ? L::swz_v(r) : L::swz_k(r);
+  const int load_swz = kValues ? L::swz_v(i * L::kLoadRows) : L::swz_k(i * L::kLoadRows);
+  const uint32_t off = uint32_t(((c ^ lane_swz) * 16 + r * L::kRowBytes) ^ (load_swz * 16));
+  // 64 lanes x 16 bytes to LDS at m0. Written out because the compiler, which cannot tell the buffers apart, would wait
+  // for every load in flight before each transposing LDS read. It has no output register; its arrival is waited for by
+  // wait_loads, which every path passes before the tile is read.
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(tile + i * 1024), "v"(off), "s"(base)
+               : "memory");
+}
+
+// Waits until at most n vector memory operations of this wave are in flight.
+template <int n>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(n >= 0 && n < 64, "6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
 
 template <typename E, int D>
-__global__ __launch_bounds__(256) void attn_kernel(AttnArgs a) {
-  __shared__ float qs[4][D], ps[4][64];
+struct Wave {
+  using L = Tile<E, D>;
+  Frag<E> q[D / 16];
+  f32x16 o[D / 32];
+  float m, c, l;     // running maximum of the scores, the same times scale2 (log2 units), sum of the weights (this half-wave's keys)
+  int32_t lo, hi;    // the keys this lane's row sees: lo <= j <= hi
+
+  __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, int hk, int32_t r, int32_t rows, int lane) {
+    const bool live = r < rows;
+    const int32_t t = live ? r / a.group : 0, g = live ? r - t * a.group : 0;
+    const uint8_t* src = a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + g) * D) * sizeof(E);
+    const int h = lane >> 5;
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      if (live)
+        q[x] = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
+      else
+        q[x].w = 0;
+    }
+    if (a.q_sign <= 0) {
+      const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kTop : 0u;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) q[x].w = (q[x].w & keep) ^ flip;
+    }
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
+    m = c = -INFINITY;
+    l = 0.0f;
+    hi = live ? max(s.kv - s.fresh + t, -1) : -1;
+    lo = a.window > 0 ? max(hi - a.window + 1, 0) : 0;
+  }
+
+  // The sum over both half-waves. A row whose scores are all NaN has no maximum: it gets one, so that it is not taken
+  // for a row that sees nothing.
+  __device__ __forceinline__ float finish() {
+    const float sum = half_sum(l);
+    if (sum != sum && c == -INFINITY) c = 0.0f;
+    return sum;
+  }
+
+  // Scores and weights of BN keys from kv0 on; `full`: every row of the wave sees them all.
+  template <int BN>
+  __device__ __forceinline__ void tile(const AttnArgs& a, const lds_u8* kt, const lds_u8* vt, int32_t kv0, bool full,
+                                       int lane) {
+    const int h = lane >> 5;
+    f32x16 s[BN / 32];
+    {
+      const int r = lane & 31;
+      const int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
+#pragma unroll
+      for (int b = 0; b < BN / 32; ++b) {
+        s[b] = 0.0f;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          Frag<E> k;
+          const lds_u8* p = kt + b * 32 * L::kRowBytes;
+          if constexpr (sizeof(E) == 2) {
+            k.w = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 32)));
+          } else {
+            const u32x4 w0 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64)));
+            const u32x4 w1 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64 + 16)));
+            k.w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
+          }
+          s[b] = mma(k, q[x], s[b]);
+        }
+      }
+    }
+    if (!full) {
+#pragma unroll
+      for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int32_t j = kv0 + b * 32 + 8 * (r / 4) + r % 4 + 4 * h;
+          if (j < lo || j > hi) s[b][r] = -INFINITY;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+    top = half_max(top);
+    if (__any(top * a.scale2 > c + kSlack)) {
+      const float m_new = fmaxf(m, top), c_new = m_new * a.scale2;
+      const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(c - c_new);
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x) o[x] *= keep;
+      l *= keep;
+      m = m_new;
+      c = c_new;
+    }
+    const float base = c == -INFINITY ? 0.0f : c;
+    Frag<E> p[BN / 16];
+    float sum = 0.0f;
+#pragma unroll
+    for (int b = 0; b < BN / 32; ++b)
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        float w[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          w[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][8 * y + r], a.scale2, -base));
+          sum += w[r];
+        }
+        p[2 * b + y] = pack(w, E{});
+      }
+    l += sum;
+    values<BN>(vt, p, kv0, full, lane);
+  }
+
+  __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int lane) const {
+    Frag<E> v;
+    const int h = lane >> 5;
+    if constexpr (sizeof(E) == 2) {
+      // lane -> row 4h + (lane % 16) / 4, columns 16 ((lane / 16) % 2) + 4 (lane % 4) ..: the transposing read hands
+      // the lane 4 rows of column lane % 32
+      const int r = 4 * h + (lane & 15) / 4;
+      const int col = 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+      const int at = r * L::kRowBytes + ((4 * x + col) ^ L::swz_v(r)) * 16 + (lane & 1) * 8 + y * 16 * L::kRowBytes;
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + at));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(vt + at + 8 * L::kRowBytes));
+      const u32x2 a = __builtin_bit_cast(u32x2, v0), b = __builtin_bit_cast(u32x2, v1);
+      v.w = __builtin_shufflevector(a, b, 0, 1, 2, 3);
+    } else {
+      const int col = 32 * x + (lane & 31);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int r = y * 16 + 8 * (j / 4) + 4 * h + j % 4;
+        const int at = r * L::kRowBytes + (((col / 4) ^ L::swz_v(r)) * 16) + (col % 4) * 4;
+        v.w[j] = *(const __attribute__((address_space(3))) uint32_t*)(vt + at);
+      }
+    }
+    return v;
+  }
+
+  template <int BN>
+  __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int32_t kv0, bool full, int lane) {
+    if (full) {
+#pragma unroll
+      for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int y = 0; y < BN / 16; ++y) o[x] = mma(value_frag(vt, x, y, lane), p[y], o[x]);
+      return;
+    }
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+#pragma unroll
+      for (int y = 0; y < BN / 16; ++y) {
+        const Frag<E> v = value_frag(vt, x, y, lane);
+        uint32_t odd = 0;
+#pragma unroll
+        for (int j = 0; j < Frag<E>::kWords; ++j) odd |= (v.w[j] & Frag<E>::kExp) + Frag<E>::kOne;
+        if (!__any((odd & Frag<E>::kTop) != 0)) {
+          o[x] = mma(v, p[y], o[x]);
+          continue;
+        }
+        float see[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int32_t j = kv0 + 16 * y + 8 * (r / 4) + r % 4 + 4 * (lane >> 5);
+          see[r] = j >= lo && j <= hi ? 1.0f : 0.0f;
+        }
+        const Frag<E> one = pack(see, E{});
+        Frag<E> fin, fu, fd;
+        split(v, fin, fu, fd);
+        o[x] = mma(fin, p[y], o[x]);
+        const f32x16 zero = 0.0f, up = mma(fu, one, zero), down = mma(fd, one, zero);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          o[x][r] += (up[r] > 0.0f ? INFINITY : 0.0f) + (down[r] > 0.0f ? -INFINITY : 0.0f);
+      }
+    }
+  }
+};
+
+template <typename E>
+__device__ __forceinline__ void store4(uint8_t* p, float a, float b, float c, float d) {
+  if constexpr (sizeof(E) == 2) {
+    u32x2 w = {f32x2_to_bf16x2(a, b), f32x2_to_bf16x2(c, d)};
+    *reinterpret_cast<u32x2*>(p) = w;
+  } else {
+    u32x4 w = {__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d)};
+    *reinterpret_cast<u32x4*>(p) = w;
+  }
+}
+
+// Output row of (sequence, key head, row), as an index of [T, Hq].
+__device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Seq& s, int hk, int32_t r) {
+  const int32_t t = r / a.group;
+  return int64_t(s.start + t) * a.Hq + hk * a.group + (r - t * a.group);
+}
+
+// A partial result: kRows rows of D floats (not normalised), then kRows maxima (log2 units) and kRows sums.
+template <int D>
+constexpr int part_floats(int rows) {
+  return rows * (D + 2);
+}
+
+// The share of the work of workgroup b: the units (sequence, key head, row
+// tile) stand in one line, each as long as its tiles of keys, and every
+// workgroup takes an equal stretch of that line, at least `least` tiles. A unit
+// that lies in one stretch is finished there; the pieces of one that is cut
+// go to `parts` (slot 0: the unit began in an earlier stretch, slot 1: it began
+// here) and the join after the cut merges them in order, so the bits do not
+// depend on timing.
+__device__ __forceinline__ int64_t stretch_of(int64_t total, int grid, int least) {
+  return max((total + grid - 1) / grid, int64_t(least));
+}
+
+// ---- few rows: at most 32 per unit (decode steps, drafts) ----
+//
+// Bound by the bytes of the cache: a unit of r rows does 4 r D flops for
+// every 4 D bytes (bf16) of keys and values, 16 flops per byte at 16 rows where
+// the card has some 250. Each wave streams tiles of 32 keys of its own
+// through its own LDS buffers without a barrier; the waves of a workgroup merge
+// at the end of a unit.
+constexpr int kNarrowRows = 32, kNarrowKeys = 32;
+
+template <typename E, int D>
+struct Narrow {
+  static constexpr int kTileBytes = kNarrowKeys * D * int(sizeof(E));
+  // two buffers of keys and values per wave in 128 KB of LDS
+  static constexpr int kWaves = kTileBytes <= 8192 ? 4 : 131072 / (4 * kTileBytes);
+  static constexpr int kThreads = kWaves * 64;
+};
+
+template <int kThreads>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t r = int64_t(blockIdx.x) * 4 + wave;
-  const int64_t t = r / a.Hq;
-  if (t >= min(max(int64_t(a.cu[a.N]), int64_t(0)), a.T)) return;
-  const int h = int(r - t * a.Hq), hk = h / (a.Hq / a.Hkv);
-  int lo = 0, hi = a.N - 1;  // the last sequence that starts at or before t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.cu[mid] <= t) lo = mid; else hi = mid - 1;
+  for (int d = 1; d < 64; d *= 2) {
+    const int64_t o = __shfl_up(v, d);
+    if (lane >= d) v += o;
   }
-  const int64_t kv = min(max(int64_t(a.kv_lens[lo]), int64_t(0)), int64_t(a.width) << a.lps);
-  const int64_t pos = kv - (int64_t(a.cu[lo + 1]) - t);
-  const int64_t first = a.window > 0 ? max(pos - a.window + 1, int64_t(0)) : 0;
-  const E* q = static_cast<const E*>(a.q) + t * a.q_stride + int64_t(h) * D;
-  for (int d = lane; d < D; d += 64) qs[wave][d] = load1(q, d);
-  float acc[D / 64] = {}, m = -INFINITY, l = 0.0f;
-  for (int64_t j0 = first; j0 <= min(pos, kv - 1); j0 += 64) {
-    const int64_t j = j0 + lane;
-    const bool seen = j <= pos && j < kv;
-    float s = -INFINITY;
-    if (seen) {
-      const int64_t page = min(max(a.table[int64_t(lo) * a.width + (j >> a.lps)], 0), a.n_pages - 1);
-      const E* k = static_cast<const E*>(a.kc) + ((((page * a.Hkv + hk) << a.lps) + (j & ((1 << a.lps) - 1))) * D);
-      float dot = 0.0f;
-      for (int d = 0; d < D; ++d) dot += qs[wave][d] * load1(k, d);
-      s = dot * a.scale;
+  __syncthreads();
+  if (lane == 63) part[wave] = v;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < kThreads / 64; ++w) {
+    if (w < wave) v += part[w];
+    total += part[w];
+  }
+  return v;
+}
+
+__device__ __forceinline__ int32_t narrow_tiles(const AttnArgs& a, int n) {
+  const Seq s = seq_of(a, n);
+  if (s.fresh == 0 || int64_t(s.fresh) * a.group > kNarrowRows) return 0;
+  const Span x = span_of<kNarrowKeys>(a, s, 0, s.fresh * a.group - 1);
+  return x.hi - x.lo;
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnArgs a) {
+  using P = Narrow<E, D>;
+  constexpr int kLoads = P::kTileBytes / 1024;
+  __shared__ __align__(1024) unsigned char buf[2 * P::kWaves * 2 * P::kTileBytes];
+  __shared__ int64_t scan_part[P::kWaves];
+  __shared__ int32_t found_seq;
+  __shared__ int64_t found_rest;
+  __shared__ float merge_c[P::kWaves][32], merge_l[P::kWaves][32];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int b = blockIdx.x;
+
+  // Total length, then the sequence that holds this stretch's start.
+  int64_t total = 0;
+  for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
+    const int n = n0 + tid;
+    int64_t sum;
+    block_scan<P::kThreads>(n < a.N ? narrow_tiles(a, n) : 0, scan_part, sum);
+    total += sum;
+  }
+  total *= a.Hkv;
+  const int64_t stretch = stretch_of(total, a.grid, P::kWaves);
+  int64_t pos = b * stretch;
+  const int64_t end = min(pos + stretch, total);
+  if (tid == 0) a.joins[4 * b + 2] = 0;
+  if (pos >= end) return;
+  {
+    int64_t before = 0;
+    for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
+      const int n = n0 + tid;
+      const int64_t t = n < a.N ? int64_t(narrow_tiles(a, n)) * a.Hkv : 0;
+      int64_t sum;
+      const int64_t inc = before + block_scan<P::kThreads>(t, scan_part, sum);
+      if (pos >= inc - t && pos < inc) {
+        found_seq = n;
+        found_rest = pos - (inc - t);
+      }
+      before += sum;
+      if (pos < before) break;
     }
-    float top = s;
-    for (int x = 32; x > 0; x /= 2) top = fmaxf(top, __shfl_xor(top, x));
-    const float m_new = fmaxf(m, top), base = m_new == -INFINITY ? 0.0f : m_new;
-    const float p = seen ? __expf(s - base) : 0.0f, keep = __expf(m - base);
-    float sum = p;
-    for (int x = 32; x > 0; x /= 2) sum += __shfl_xor(sum, x);
-    l = l * keep + sum;
-    m = m_new;
-    ps[wave][lane] = p;
-    for (int c = 0; c < D / 64; ++c) acc[c] *= keep;
-    const int n = int(min(int64_t(64), min(pos, kv - 1) - j0 + 1));
-    for (int x = 0; x < n; ++x) {
-      const int64_t jj = j0 + x;
-      const int64_t page = min(max(a.table[int64_t(lo) * a.width + (jj >> a.lps)], 0), a.n_pages - 1);
-      const E* v = static_cast<const E*>(a.vc) + ((((page * a.Hkv + hk) << a.lps) + (jj & ((1 << a.lps) - 1))) * D);
-      for (int c = 0; c < D / 64; ++c) acc[c] += ps[wave][x] * load1(v, c * 64 + lane);
+    __syncthreads();
+  }
+  int n = __builtin_amdgcn_readfirstlane(found_seq);
+  int64_t rest = found_rest;   // position within the sequence's units
+  Wave<E, D> w;
+  lds_u8* const mine = (lds_u8*)buf + wave * 4 * P::kTileBytes;
+  while (pos < end && n < a.N) {
+    const Seq s = seq_of(a, n);
+    const int32_t rows = int64_t(s.fresh) * a.group > kNarrowRows ? 0 : s.fresh * a.group;
+    if (rows == 0) {
+      ++n;
+      continue;
+    }
+    const Span x = span_of<kNarrowKeys>(a, s, 0, rows - 1);
+    const int32_t tiles = x.hi - x.lo;
+    const int hk = __builtin_amdgcn_readfirstlane(int(rest / tiles));
+    const int32_t t0 = int32_t(rest - int64_t(hk) * tiles);
+    const int32_t t1 = int32_t(min(int64_t(tiles), t0 + (end - pos)));
+    const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
+    const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
+    w.start(a, s, hk, lane & 31, rows, lane);
+
+    auto load = [&](int32_t t, uint32_t to) {
+      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_rows<E, D, false>(a, a.kc, row, hk, kv0, last_page, i, to, lane);
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, i, to + P::kTileBytes, lane);
+    };
+    uint32_t half = 0;
+    wait_loads<0>();   // no store of the unit before is counted below
+    if (t0 + wave < t1) load(t0 + wave, uint32_t(uintptr_t(mine)));
+    for (int32_t t = t0 + wave; t < t1; t += P::kWaves) {
+      if (t + P::kWaves < t1) {
+        load(t + P::kWaves, uint32_t(uintptr_t(mine)) + (half ^ 2 * P::kTileBytes));
+        wait_loads<(2 * kLoads < 63 ? 2 * kLoads : 63)>();   // all but the loads just issued
+      } else {
+        wait_loads<0>();
+      }
+      const int32_t kv0 = (x.lo + t) * kNarrowKeys;
+      const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
+      w.template tile<kNarrowKeys>(a, mine + half, mine + half + P::kTileBytes, kv0, full, lane);
+      half ^= 2 * P::kTileBytes;
+    }
+
+    // The waves merge: maxima and sums first, then every thread sums some columns over the waves.
+    const float l_all = w.finish();
+    __syncthreads();   // the buffers are free
+    float* const sums = reinterpret_cast<float*>(buf);
+    const int q = lane & 31, h = lane >> 5;
+    if (h == 0) {
+      merge_c[wave][q] = w.c;
+      merge_l[wave][q] = l_all;
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == tiles;
+    float* const part = a.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
+    // a half of the columns at a time: the merge buffer is one of the two stages
+#pragma unroll
+    for (int x0 = 0; x0 < D / 32; x0 += (D / 32 + 1) / 2) {
+      constexpr int kX = (D / 32 + 1) / 2, kC = kX * 32, kRow = kC + 4;  // 4 floats against bank conflicts
+      static_assert(P::kWaves * 32 * kRow * 4 <= int(sizeof(buf)), "merge buffer");
+      if (q < rows) {
+#pragma unroll
+        for (int y = 0; y < kX; ++y)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const f32x16& v = w.o[x0 + y];
+            float4 f = {v[4 * r], v[4 * r + 1], v[4 * r + 2], v[4 * r + 3]};
+            *reinterpret_cast<float4*>(sums + (wave * 32 + q) * kRow + y * 32 + 8 * r + 4 * h) = f;
+          }
+      }
+      __syncthreads();
+      for (int e = tid; e < rows * (kC / 4); e += P::kThreads) {
+        const int qq = e / (kC / 4), d = (e % (kC / 4)) * 4;
+        float top = -INFINITY;
+        for (int v = 0; v < P::kWaves; ++v) top = fmaxf(top, merge_c[v][qq]);
+        const float base = top == -INFINITY ? 0.0f : top;
+        float4 acc = {0, 0, 0, 0};
+        float l = 0.0f;
+        for (int v = 0; v < P::kWaves; ++v) {
+          const float f = __builtin_amdgcn_exp2f(merge_c[v][qq] - base);
+          const float4 z = *reinterpret_cast<const float4*>(sums + (v * 32 + qq) * kRow + d);
+          if (merge_c[v][qq] != -INFINITY) {
+            acc.x += f * z.x;
+            acc.y += f * z.y;
+            acc.z += f * z.z;
+            acc.w += f * z.w;
+            l += f * merge_l[v][qq];
+          }
+        }
+        const int col = x0 * 32 + d;
+        if (whole) {
+          const float inv = top == -INFINITY ? 0.0f : 1.0f / l;
+          const int64_t r = out_row(a, s, hk, qq);
+          store4<E>(a.o + (r * D + col) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+          if (a.lse != nullptr && col == 0) a.lse[r] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * kLn2;
+        } else {
+          *reinterpret_cast<float4*>(part + qq * D + col) = acc;
+          if (col == 0) {
+            part[kNarrowRows * D + qq] = top;
+            part[kNarrowRows * (D + 1) + qq] = l;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (tid == 0 && t0 > 0 && b * stretch == pos && pos - t0 >= (b - 1) * stretch) {
+      // the first cut of this unit: it began in the stretch before
+      a.joins[4 * b] = n;
+      a.joins[4 * b + 1] = hk;
+      a.joins[4 * b + 3] = 0;
+      a.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+    }
+    pos += t1 - t0;
+    rest = t1 < tiles ? rest + (t1 - t0) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * tiles : 0);
+    if (t1 == tiles && hk + 1 == a.Hkv) ++n;
+  }
+}
+
+// Merges the pieces of a unit that was cut, one row per D / 4 threads, in the order of the keys.
+template <typename E, int D, int kRows>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
+  constexpr int kLanes = D / 4, kSets = 256 / kLanes;   // threads of a row, pieces read side by side
+  __shared__ float4 acc_s[kSets][kLanes];
+  __shared__ float l_s[kSets], c_s[kSets];
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int pieces = a.joins[4 * b + 2];
+  if (pieces == 0) return;
+  const int n = a.joins[4 * b], hk = a.joins[4 * b + 1], r0 = a.joins[4 * b + 3];
+  const Seq s = seq_of(a, n);
+  const int set = tid / kLanes, d = (tid % kLanes) * 4;
+  for (int q = blockIdx.y; q < kRows && r0 + q < s.fresh * a.group; q += gridDim.y) {
+    float4 acc = {0, 0, 0, 0};
+    float l = 0.0f, c = -INFINITY;
+    for (int i = set; i < pieces; i += kSets) {
+      const float* part = a.parts + int64_t(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)) * part_floats<D>(kRows);
+      const float pc = part[kRows * D + q], pl = part[kRows * (D + 1) + q];
+      const float4 z = *reinterpret_cast<const float4*>(part + q * D + d);
+      if (pc != -INFINITY) {
+        const float top = fmaxf(c, pc), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc - top);
+        acc.x = acc.x * f0 + z.x * f1;
+        acc.y = acc.y * f0 + z.y * f1;
+        acc.z = acc.z * f0 + z.z * f1;
+        acc.w = acc.w * f0 + z.w * f1;
+        l = l * f0 + pl * f1;
+        c = top;
+      }
+    }
+    acc_s[set][tid % kLanes] = acc;
+    if (d == 0) l_s[set] = l, c_s[set] = c;
+    __syncthreads();
+    if (set == 0) {
+      float top = -INFINITY;
+      for (int v = 0; v < kSets; ++v) top = fmaxf(top, c_s[v]);
+      float4 sum = {0, 0, 0, 0};
+      float ls = 0.0f;
+      for (int v = 0; v < kSets; ++v)
+        if (c_s[v] != -INFINITY) {
+          const float f = __builtin_amdgcn_exp2f(c_s[v] - top);
+          const float4 z = acc_s[v][tid];
+          sum.x += f * z.x;
+          sum.y += f * z.y;
+          sum.z += f * z.z;
+          sum.w += f * z.w;
+          ls += f * l_s[v];
+        }
+      const float inv = top == -INFINITY ? 0.0f : 1.0f / ls;
+      const int64_t r = out_row(a, s, hk, r0 + q);
+      store4<E>(a.o + (r * D + d) * sizeof(E), sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+      if (a.lse != nullptr && d == 0) a.lse[r] = top == -INFINITY ? -INFINITY : (top + log2f(ls)) * kLn2;
+    }
+    __syncthreads();
+  }
+}
+
+// ---- many rows: chunks of a prompt, and whatever stands beside them in a batch ----
+//
+// Bound by the matrix cores. kRows rows of one (sequence, key head) share
+// every tile of kKeys keys and values, which the waves fetch together into one of two LDS
+// buffers while they work on the other; one barrier a tile.
+template <typename E, int D>
+struct Wide {
+  static constexpr int kWaves = D * int(sizeof(E)) <= 256 ? 8 : 4;
+  static constexpr int kThreads = kWaves * 64;
+  static constexpr int kRows = kWaves * 32;
+  static constexpr int kKeys = D * int(sizeof(E)) <= 512 ? 64 : 32;
+  static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
+  static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
+};
+
+// The row tiles of all sequences: sched[0] their number, sched[1] the tiles of
+// keys of one key head, then for each the tiles before it and (sequence << 32 | row tile).
+constexpr int kSchedThreads = 1024;
+
+template <int kRows, int kKeys>
+__global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
+  __shared__ int64_t part[kSchedThreads / 64];
+  const int tid = threadIdx.x;
+  int64_t* const before = a.sched + 2;
+  int64_t* const which = before + a.max_tiles;
+  int64_t* const starts = which + a.max_tiles;   // row tiles before each sequence
+  int64_t count = 0, sum;
+  for (int n0 = 0; n0 < a.N; n0 += kSchedThreads) {
+    const int n = n0 + tid;
+    const int64_t v = n < a.N ? (int64_t(seq_of(a, n).fresh) * a.group + kRows - 1) / kRows : 0;
+    const int64_t inc = count + block_scan<kSchedThreads>(v, part, sum);
+    if (n < a.N) starts[n] = inc - v;
+    count += sum;
+  }
+  count = min(count, int64_t(a.max_tiles));
+  __syncthreads();
+  int64_t total = 0;
+  for (int64_t t0 = 0; t0 < count; t0 += kSchedThreads) {
+    const int64_t t = t0 + tid;
+    int64_t v = 0;
+    if (t < count) {
+      int lo = 0, hi = a.N - 1;  // the last sequence that starts at or before t; empty ones share their start with the next
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const Seq s = seq_of(a, lo);
+      const int32_t r0 = int32_t(t - starts[lo]) * kRows;
+      const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
+      v = x.hi - x.lo;
+      which[t] = int64_t(lo) << 32 | (t - starts[lo]);
+    }
+    const int64_t inc = total + block_scan<kSchedThreads>(v, part, sum);
+    if (t < count) before[t] = inc - v;
+    total += sum;
+  }
+  if (tid == 0) {
+    a.sched[0] = count;
+    a.sched[1] = total;
+  }
+}
+
+template <typename E, int D>
+__global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
+  using P = Wide<E, D>;
+  __shared__ __align__(1024) unsigned char buf[4 * P::kTileBytes];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
+  const int b = int(blockIdx.x % 8) * (a.grid / 8) + int(blockIdx.x / 8);
+  const int64_t count = a.sched[0], per_head = a.sched[1];
+  const int64_t total = per_head * a.Hkv;
+  const int64_t stretch = stretch_of(total, a.grid, 1);
+  int64_t pos = b * stretch;
+  const int64_t end = min(pos + stretch, total);
+  if (tid == 0) a.joins[4 * b + 2] = 0;
+  if (pos >= end) return;
+  const int64_t* const before = a.sched + 2;
+  const int64_t* const which = before + a.max_tiles;
+  int hk = __builtin_amdgcn_readfirstlane(int(pos / per_head));
+  int64_t rest = pos - hk * per_head;
+  int rt;
+  {
+    // the last row tile that starts at or before `rest`, 64 probes at a time
+    int64_t lo = 0, len = count;
+    while (len > 1) {
+      const int64_t step = (len + 63) / 64, at = lo + lane * step;
+      const int hits = __popcll(__ballot(at < lo + len && before[min(at, count - 1)] <= rest));
+      const int64_t next = lo + max(hits - 1, 0) * step;
+      len = min(step, lo + len - next);
+      lo = next;
+    }
+    rt = __builtin_amdgcn_readfirstlane(int(lo));
+    rest -= before[rt];
+  }
+  Wave<E, D> w;
+  lds_u8* const tiles_at = (lds_u8*)buf;
+  while (pos < end) {
+    const int64_t id = which[rt];
+    const int n = __builtin_amdgcn_readfirstlane(int(id >> 32));
+    const Seq s = seq_of(a, n);
+    const int32_t rows = s.fresh * a.group;
+    const int32_t r0 = __builtin_amdgcn_readfirstlane(int(id & 0xFFFFFFFF)) * P::kRows;
+    const Span x = span_of<P::kKeys>(a, s, r0, max(min(r0 + P::kRows, rows) - 1, r0));
+    const int32_t tiles = x.hi - x.lo;
+    const int32_t t0 = __builtin_amdgcn_readfirstlane(int32_t(rest));
+    const int32_t t1 = __builtin_amdgcn_readfirstlane(int32_t(min(int64_t(tiles), t0 + (end - pos))));
+    const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
+    const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
+    const int32_t w0 = r0 + wave * 32;   // this wave's rows
+    const bool busy = w0 < rows;
+    const Span mine = span_of<P::kKeys>(a, s, min(w0, rows - 1), min(w0 + 31, rows - 1));
+    w.start(a, s, hk, w0 + (lane & 31), rows, lane);
+
+    auto load = [&](int32_t t, uint32_t to) {
+      const int32_t kv0 = (x.lo + t) * P::kKeys;
+#pragma unroll
+      for (int i = 0; i < P::kLoads; ++i)
+        load_rows<E, D, false>(a, a.kc, row, hk, kv0, last_page, wave * P::kLoads + i, to, lane);
+#pragma unroll
+      for (int i = 0; i < P::kLoads; ++i)
+        load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, wave * P::kLoads + i, to + P::kTileBytes, lane);
+    };
+    uint32_t half = 0;
+    load(t0, uint32_t(uintptr_t(tiles_at)));
+    for (int32_t t = t0; t < t1; ++t) {
+      wait_loads<0>();
+      __syncthreads();   // the tile is there, and every wave is done with the other buffer
+      if (t + 1 < t1) load(t + 1, uint32_t(uintptr_t(tiles_at)) + (half ^ 2 * P::kTileBytes));
+      const int32_t kv0 = (x.lo + t) * P::kKeys;
+      const bool none = !busy || kv0 > mine.last || (a.window > 0 && kv0 + P::kKeys - 1 <= mine.first - a.window);
+      const bool full = kv0 + P::kKeys - 1 <= mine.first && (a.window == 0 || kv0 > mine.last - a.window);
+      if (!none)
+        w.template tile<P::kKeys>(a, tiles_at + half, tiles_at + half + P::kTileBytes, kv0, full, lane);
+      half ^= 2 * P::kTileBytes;
+    }
+    __syncthreads();   // before the next unit's loads
+
+    const float l_all = w.finish();
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int32_t r = w0 + (lane & 31), h = lane >> 5;
+    if (whole) {
+      if (r < rows) {
+        const float inv = w.c == -INFINITY ? 0.0f : 1.0f / l_all;
+        const int64_t at = out_row(a, s, hk, r);
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            store4<E>(a.o + (at * D + y * 32 + 8 * k + 4 * h) * sizeof(E), w.o[y][4 * k] * inv, w.o[y][4 * k + 1] * inv,
+                      w.o[y][4 * k + 2] * inv, w.o[y][4 * k + 3] * inv);
+        if (a.lse != nullptr && h == 0) a.lse[at] = w.c == -INFINITY ? -INFINITY : (w.c + log2f(l_all)) * kLn2;
+      }
+    } else {
+      float* const part = a.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(P::kRows);
+      const int q = wave * 32 + (lane & 31);
+      if (r < rows) {
+#pragma unroll
+        for (int y = 0; y < D / 32; ++y)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 f = {w.o[y][4 * k], w.o[y][4 * k + 1], w.o[y][4 * k + 2], w.o[y][4 * k + 3]};
+            *reinterpret_cast<float4*>(part + q * D + y * 32 + 8 * k + 4 * h) = f;
+          }
+        if (h == 0) {
+          part[P::kRows * D + q] = w.c;
+          part[P::kRows * (D + 1) + q] = l_all;
+        }
+      }
+      if (tid == 0 && t0 > 0 && pos == b * stretch && pos - t0 >= (b - 1) * stretch) {
+        a.joins[4 * b] = n;
+        a.joins[4 * b + 1] = hk;
+        a.joins[4 * b + 3] = r0;
+        a.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+      }
+    }
+    pos += t1 - t0;
+    rest = 0;
+    if (++rt >= count) {
+      rt = 0;
+      ++hk;
     }
   }
-  E* o = static_cast<E*>(a.o) + r * D;
-  const float inv = m == -INFINITY ? 0.0f : 1.0f / l;
-  for (int c = 0; c < D / 64; ++c) store1(o, c * 64 + lane, m == -INFINITY ? 0.0f : acc[c] * inv);
-  if (a.lse != nullptr && lane == 0) a.lse[r] = m == -INFINITY ? -INFINITY : m + logf(l);
 }
 
 rglru_status_t check(const rglru_paged_shape_t& s) {
@@ -95,13 +886,80 @@ rglru_status_t check(const rglru_paged_shape_t& s) {
   return RGLRU_OK;
 }
 
-template <typename E>
-void launch(const AttnArgs& a, int dim, hipStream_t st) {
-  const unsigned grid = unsigned(ceil_div(a.T * a.Hq, 4));
-  if (dim == 64) attn_kernel<E, 64><<<grid, 256, 0, st>>>(a);
-  else if (dim == 128) attn_kernel<E, 128><<<grid, 256, 0, st>>>(a);
-  else attn_kernel<E, 256><<<grid, 256, 0, st>>>(a);
+// The largest number of rows of one sequence that the caller allows.
+int64_t most_rows(const rglru_paged_shape_t& s) {
+  const int64_t longest = s.max_new > 0 && s.max_new < s.n_tokens ? s.max_new : s.n_tokens;
+  return longest * (s.q_heads / s.kv_heads);
 }
+
+struct Plan {
+  bool narrow;
+  int grid;             // workgroups, a multiple of 8
+  int64_t max_tiles;    // row tiles at most (wide)
+  size_t joins, parts, bytes;  // offsets and size of the workspace
+};
+
+template <typename E, int D>
+Plan plan_of(const rglru_paged_shape_t& s) {
+  Plan p;
+  p.narrow = most_rows(s) <= kNarrowRows;
+  const int64_t group = s.q_heads / s.kv_heads;
+  const int64_t keys = int64_t(s.max_pages) * s.page_size;
+  const int64_t seqs = s.n_seqs < s.n_tokens ? s.n_seqs : s.n_tokens;
+  int64_t units, tiles;  // upper bounds on units and on the tiles of one
+  if (p.narrow) {
+    units = seqs * s.kv_heads;
+    tiles = ceil_div(ceil_div(keys, kNarrowKeys), Narrow<E, D>::kWaves);
+    p.max_tiles = 0;
+  } else {
+    p.max_tiles = ceil_div(s.n_tokens * group, Wide<E, D>::kRows) + seqs;
+    units = p.max_tiles * s.kv_heads;
+    tiles = ceil_div(keys, Wide<E, D>::kKeys);
+  }
+  const int64_t most = 256;
+  int64_t grid = units >= most || tiles >= most ? most : units * tiles;
+  if (grid > most) grid = most;
+  p.grid = int((grid + 7) / 8 * 8);
+  const int rows = p.narrow ? kNarrowRows : Wide<E, D>::kRows;
+  const size_t sched = p.narrow ? 0 : round_up(size_t(2 + 2 * p.max_tiles + s.n_seqs) * 8, 256);
+  p.joins = sched;
+  p.parts = p.joins + round_up(size_t(p.grid) * 16, 256);
+  p.bytes = p.parts + size_t(p.grid) * 2 * part_floats<D>(rows) * 4;
+  return p;
+}
+
+template <typename E, int D>
+size_t bytes_of(const rglru_paged_shape_t& s) {
+  return plan_of<E, D>(s).bytes;
+}
+
+template <typename E, int D>
+void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStream_t st) {
+  const Plan p = plan_of<E, D>(s);
+  a.sched = reinterpret_cast<int64_t*>(workspace);
+  a.joins = reinterpret_cast<int32_t*>(workspace + p.joins);
+  a.parts = reinterpret_cast<float*>(workspace + p.parts);
+  a.grid = p.grid;
+  a.max_tiles = int32_t(p.max_tiles);
+  const int64_t most = most_rows(s);
+  if (p.narrow) {
+    narrow_kernel<E, D><<<unsigned(p.grid), Narrow<E, D>::kThreads, 0, st>>>(a);
+    join_kernel<E, D, kNarrowRows><<<dim3(unsigned(p.grid), unsigned(most)), 256, 0, st>>>(a);
+  } else {
+    using P = Wide<E, D>;
+    sched_kernel<P::kRows, P::kKeys><<<1, kSchedThreads, 0, st>>>(a);
+    wide_kernel<E, D><<<unsigned(p.grid), P::kThreads, 0, st>>>(a);
+    join_kernel<E, D, P::kRows><<<dim3(unsigned(p.grid), P::kRows / 8), 256, 0, st>>>(a);
+  }
+}
+
+// Calls f<E, D>(...) for the shape's type and head width.
+#define RGLRU_PAGED_DISPATCH(s, f, ...)                                                                  \
+  ((s).io_dtype == RGLRU_IO_BF16                                                                         \
+       ? ((s).head_dim == 64 ? f<uint16_t, 64>(__VA_ARGS__)                                              \
+                             : (s).head_dim == 128 ? f<uint16_t, 128>(__VA_ARGS__) : f<uint16_t, 256>(__VA_ARGS__)) \
+       : ((s).head_dim == 64 ? f<float, 64>(__VA_ARGS__)                                                 \
+                             : (s).head_dim == 128 ? f<float, 128>(__VA_ARGS__) : f<float, 256>(__VA_ARGS__)))
 
 }  // namespace
 }  // namespace paged
@@ -111,7 +969,7 @@ using namespace rglru;
 
 extern "C" size_t rglru_paged_attn_workspace_bytes(const rglru_paged_shape_t* sp) {
   if (sp == nullptr || paged::check(*sp) != RGLRU_OK) return 0;
-  return 256;
+  return RGLRU_PAGED_DISPATCH(*sp, paged::bytes_of, *sp);
 }
 
 extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, const int32_t* cu_seqlens,
@@ -138,10 +996,10 @@ extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, co
   a.cu = cu_seqlens;
   a.kv_lens = kv_lens;
   a.table = block_table;
-  a.q = q;
-  a.kc = k_cache;
-  a.vc = v_cache;
-  a.o = o;
+  a.q = static_cast<const uint8_t*>(q);
+  a.kc = static_cast<const uint8_t*>(k_cache);
+  a.vc = static_cast<const uint8_t*>(v_cache);
+  a.o = static_cast<uint8_t*>(o);
   a.lse = lse;
   a.T = s.n_tokens;
   a.q_stride = stride;
@@ -151,9 +1009,10 @@ extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, co
   a.lps = paged::log2_of(s.page_size);
   a.Hq = s.q_heads;
   a.Hkv = s.kv_heads;
-  a.window = s.window;
-  a.scale = s.scale;
-  if (s.io_dtype == RGLRU_IO_BF16) paged::launch<uint16_t>(a, s.head_dim, static_cast<hipStream_t>(stream));
-  else paged::launch<float>(a, s.head_dim, static_cast<hipStream_t>(stream));
+  a.group = s.q_heads / s.kv_heads;
+  a.window = s.window < int64_t(s.max_pages) * s.page_size ? s.window : 0;  // a window as long as the row hides nothing
+  a.scale2 = s.scale == 0.0f ? 1.0f : std::fabs(s.scale) * paged::kLog2e;
+  a.q_sign = s.scale > 0.0f ? 1 : s.scale < 0.0f ? -1 : 0;
+  RGLRU_PAGED_DISPATCH(s, paged::launch, s, a, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream));
   return launch_status();
 }
