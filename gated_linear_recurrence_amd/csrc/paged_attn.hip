@@ -22,10 +22,12 @@
 //
 // What a row must not see must not reach it, infinities and NaN included:
 // scores are replaced where they are masked, but a weight of 0 times an
-// infinite value is NaN. Tiles that some row of the wave does not see in full
-// therefore look at their values first; where one is not finite, the product
-// runs on the values with those replaced by 0, and two further products of
-// 0/1 operands tell which (row, column) pairs see a +inf, a -inf or a NaN.
+// infinite value is NaN. The values of a tile that some row does not see in
+// full are therefore looked at first; where one is not finite, products of 0/1
+// operands mark the (row, column) pairs that see a +inf, a -inf or a NaN, and
+// those values are replaced by 0 in LDS before the tile is worked on.
+#include <cfloat>
+
 #include <hip/hip_runtime.h>
 
 #include "paged_common.h"
@@ -54,13 +56,13 @@ struct Frag;
 template <>
 struct Frag<uint16_t> {
   static constexpr int kWords = 4;
-  static constexpr uint32_t kExp = 0x7F807F80u, kOne = 0x00800080u, kTop = 0x80008000u;
+  static constexpr uint32_t kSigns = 0x80008000u;
   u32x4 w;
 };
 template <>
 struct Frag<float> {
   static constexpr int kWords = 8;
-  static constexpr uint32_t kExp = 0x7F800000u, kOne = 0x00800000u, kTop = 0x80000000u;
+  static constexpr uint32_t kSigns = 0x80000000u;
   u32x8 w;
 };
 
@@ -88,34 +90,39 @@ __device__ __forceinline__ Frag<float> pack(const float* p, float) {
   return f;
 }
 
-// Splits an operand into its finite elements and 0/1 operands marking +inf or NaN, and -inf or NaN.
-__device__ __forceinline__ void split(const Frag<uint16_t>& f, Frag<uint16_t>& fin, Frag<uint16_t>& up,
-                                      Frag<uint16_t>& down) {
+// The elements of a word that are not finite (bf16 pairs or a float), all their bits set.
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w, uint16_t) {
+  const uint32_t top = (((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u;
+  return (top << 16) - top;
+}
+__device__ __forceinline__ uint32_t odd_bits(uint32_t w, float) {
+  return (w & 0x7F800000u) == 0x7F800000u ? ~0u : 0u;
+}
+
+// A 0/1 operand that marks +inf and NaN (sign 0) or -inf and NaN (sign 1).
+__device__ __forceinline__ Frag<uint16_t> marks(const Frag<uint16_t>& f, uint32_t sign) {
+  Frag<uint16_t> m;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t c = 0, u = 0, d = 0;
+    uint32_t w = 0;
 #pragma unroll
     for (int s = 0; s < 32; s += 16) {
       const uint32_t x = (f.w[j] >> s) & 0xFFFFu;
-      const bool odd = (x & 0x7F80u) == 0x7F80u, nan = odd && (x & 0x7Fu) != 0;
-      c |= (odd ? 0u : x) << s;
-      u |= (odd && (nan || x == 0x7F80u) ? 0x3F80u : 0u) << s;
-      d |= (odd && (nan || x == 0xFF80u) ? 0x3F80u : 0u) << s;
+      const bool nan = (x & 0x7FFFu) > 0x7F80u;
+      w |= (nan || x == (sign << 15 | 0x7F80u) ? 0x3F80u : 0u) << s;
     }
-    fin.w[j] = c;
-    up.w[j] = u;
-    down.w[j] = d;
+    m.w[j] = w;
   }
+  return m;
 }
-__device__ __forceinline__ void split(const Frag<float>& f, Frag<float>& fin, Frag<float>& up, Frag<float>& down) {
+__device__ __forceinline__ Frag<float> marks(const Frag<float>& f, uint32_t sign) {
+  Frag<float> m;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t x = f.w[j];
-    const bool odd = (x & 0x7F800000u) == 0x7F800000u, nan = odd && (x & 0x7FFFFFu) != 0;
-    fin.w[j] = odd ? 0u : x;
-    up.w[j] = odd && (nan || x == 0x7F800000u) ? 0x3F800000u : 0u;
-    down.w[j] = odd && (nan || x == 0xFF800000u) ? 0x3F800000u : 0u;
+    const bool nan = (f.w[j] & 0x7FFFFFFFu) > 0x7F800000u;
+    m.w[j] = nan || f.w[j] == (sign << 31 | 0x7F800000u) ? 0x3F800000u : 0u;
   }
+  return m;
 }
 
 __device__ __forceinline__ float half_max(float x) {
@@ -244,7 +251,7 @@ struct Wave {
         q[x].w = 0;
     }
     if (a.q_sign <= 0) {
-      const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kTop : 0u;
+      const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) q[x].w = (q[x].w & keep) ^ flip;
     }
@@ -308,7 +315,8 @@ struct Wave {
     top = half_max(top);
     if (__any(top * a.scale2 > c + kSlack)) {
       const float m_new = fmaxf(m, top), c_new = m_new * a.scale2;
-      const float keep = m_new == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(c - c_new);
+      // never 0, so that an infinite output stays one (the smallest float leaves nothing else behind)
+      const float keep = c == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(c - c_new), FLT_MIN);
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) o[x] *= keep;
       l *= keep;
@@ -331,7 +339,10 @@ struct Wave {
         p[2 * b + y] = pack(w, E{});
       }
     l += sum;
-    values<BN>(vt, p, kv0, full, lane);
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+      for (int y = 0; y < BN / 16; ++y) o[x] = mma(value_frag(vt, x, y, lane), p[y], o[x]);
   }
 
   __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int lane) const {
@@ -360,45 +371,57 @@ struct Wave {
     return v;
   }
 
+  // Marks what values that are not finite do to this wave's rows: a row that sees a +inf or a NaN gets +inf in its
+  // column, one that sees a -inf or a NaN gets -inf (so NaN gives NaN). Products of 0/1 operands, which are finite.
   template <int BN>
-  __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int32_t kv0, bool full, int lane) {
-    if (full) {
+  __device__ __forceinline__ void mark(const lds_u8* vt, int32_t kv0, int lane) {
+    Frag<E> see[BN / 16];
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x)
+    for (int y = 0; y < BN / 16; ++y) {
+      float one[8];
 #pragma unroll
-        for (int y = 0; y < BN / 16; ++y) o[x] = mma(value_frag(vt, x, y, lane), p[y], o[x]);
-      return;
-    }
-#pragma unroll
-    for (int x = 0; x < D / 32; ++x) {
-#pragma unroll
-      for (int y = 0; y < BN / 16; ++y) {
-        const Frag<E> v = value_frag(vt, x, y, lane);
-        uint32_t odd = 0;
-#pragma unroll
-        for (int j = 0; j < Frag<E>::kWords; ++j) odd |= (v.w[j] & Frag<E>::kExp) + Frag<E>::kOne;
-        if (!__any((odd & Frag<E>::kTop) != 0)) {
-          o[x] = mma(v, p[y], o[x]);
-          continue;
-        }
-        float see[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int32_t j = kv0 + 16 * y + 8 * (r / 4) + r % 4 + 4 * (lane >> 5);
-          see[r] = j >= lo && j <= hi ? 1.0f : 0.0f;
-        }
-        const Frag<E> one = pack(see, E{});
-        Frag<E> fin, fu, fd;
-        split(v, fin, fu, fd);
-        o[x] = mma(fin, p[y], o[x]);
-        const f32x16 zero = 0.0f, up = mma(fu, one, zero), down = mma(fd, one, zero);
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          o[x][r] += (up[r] > 0.0f ? INFINITY : 0.0f) + (down[r] > 0.0f ? -INFINITY : 0.0f);
+      for (int r = 0; r < 8; ++r) {
+        const int32_t j = kv0 + 16 * y + 8 * (r / 4) + r % 4 + 4 * (lane >> 5);
+        one[r] = j >= lo && j <= hi ? 1.0f : 0.0f;
       }
+      see[y] = pack(one, E{});
     }
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+#pragma unroll 1
+      for (uint32_t sign = 0; sign < 2; ++sign) {
+        f32x16 sum = 0.0f;
+#pragma unroll
+        for (int y = 0; y < BN / 16; ++y) sum = mma(marks(value_frag(vt, x, y, lane), sign), see[y], sum);
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[x][r] += sum[r] > 0.0f ? (sign ? -INFINITY : INFINITY) : 0.0f;
+      }
   }
 };
+
+// Whether this thread's share of a tile of values holds one that is not finite.
+template <typename E, int kTileBytes, int kThreads>
+__device__ __forceinline__ bool any_odd(const lds_u8* vt, int thread) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int i = thread * 16; i < kTileBytes; i += kThreads * 16) {
+    const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) odd |= odd_bits(w[j], E{});
+  }
+  return odd != 0;
+}
+
+// Replaces them by 0.
+template <typename E, int kTileBytes, int kThreads>
+__device__ __forceinline__ void clean(lds_u8* vt, int thread) {
+  for (int i = thread * 16; i < kTileBytes; i += kThreads * 16) {
+    u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] &= ~odd_bits(w[j], E{});
+    *(__attribute__((address_space(3))) u32x4*)(vt + i) = w;
+  }
+}
 
 template <typename E>
 __device__ __forceinline__ void store4(uint8_t* p, float a, float b, float c, float d) {
@@ -557,6 +580,10 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       }
       const int32_t kv0 = (x.lo + t) * kNarrowKeys;
       const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
+      if (!full && __any(any_odd<E, P::kTileBytes, 64>(mine + half + P::kTileBytes, lane))) {
+        w.template mark<kNarrowKeys>(mine + half + P::kTileBytes, kv0, lane);
+        clean<E, P::kTileBytes, 64>(mine + half + P::kTileBytes, lane);
+      }
       w.template tile<kNarrowKeys>(a, mine + half, mine + half + P::kTileBytes, kv0, full, lane);
       half ^= 2 * P::kTileBytes;
     }
@@ -758,6 +785,7 @@ template <typename E, int D>
 __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
   using P = Wide<E, D>;
   __shared__ __align__(1024) unsigned char buf[4 * P::kTileBytes];
+  __shared__ int odd_waves[P::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
   const int b = int(blockIdx.x % 8) * (a.grid / 8) + int(blockIdx.x / 8);
@@ -823,6 +851,21 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
       const int32_t kv0 = (x.lo + t) * P::kKeys;
       const bool none = !busy || kv0 > mine.last || (a.window > 0 && kv0 + P::kKeys - 1 <= mine.first - a.window);
       const bool full = kv0 + P::kKeys - 1 <= mine.first && (a.window == 0 || kv0 > mine.last - a.window);
+      if (kv0 + P::kKeys - 1 > x.first || (a.window > 0 && kv0 <= x.last - a.window)) {
+        // some row of the workgroup does not see all of it
+        lds_u8* const vt = tiles_at + half + P::kTileBytes;
+        const bool odd = __any(any_odd<E, P::kTileBytes, P::kThreads>(vt, tid));
+        if (lane == 0) odd_waves[wave] = odd;
+        __syncthreads();
+        int found = 0;
+        for (int v = 0; v < P::kWaves; ++v) found |= odd_waves[v];
+        if (found) {
+          if (!none) w.template mark<P::kKeys>(vt, kv0, lane);
+          __syncthreads();
+          clean<E, P::kTileBytes, P::kThreads>(vt, tid);
+          __syncthreads();
+        }
+      }
       if (!none)
         w.template tile<P::kKeys>(a, tiles_at + half, tiles_at + half + P::kTileBytes, kv0, full, lane);
       half ^= 2 * P::kTileBytes;
