@@ -154,6 +154,13 @@ struct Tile {
   }
 };
 
+// What one kernel leaves for the join.
+struct Cuts {
+  int32_t* joins;  // [grid][4]: sequence, key head, pieces (0: none) and first row of what the cut before workgroup b parted
+  float* parts;    // [grid][2]: partial results of a workgroup's first and last unit
+  int32_t grid;
+};
+
 struct AttnArgs {
   const int32_t* cu;
   const int32_t* kv_lens;
@@ -163,11 +170,11 @@ struct AttnArgs {
   const uint8_t* vc;
   uint8_t* o;
   float* lse;
-  int64_t* sched;   // wide calls: the row tiles (see sched_kernel)
-  int32_t* joins;   // [grid][4]: what the join after workgroup b merges
-  float* parts;     // [grid][2]: partial results of a workgroup's first and last unit
+  int64_t* sched;   // the row tiles of the wide kernel (see sched_kernel)
+  Cuts narrow, wide;
   int64_t T, q_stride;
-  int32_t n_pages, N, width, lps, Hq, Hkv, group, window, grid, max_tiles;
+  int32_t n_pages, N, width, lps, Hq, Hkv, group, window, max_tiles;
+  int32_t least_rows;  // the wide kernel's sequences have more rows than this
   float scale2;     // |scale| log2 e (1 for a scale of 0, whose queries are zeroed)
   int32_t q_sign;   // sign of the scale: -1, 0, 1
 };
@@ -222,18 +229,28 @@ __device__ __forceinline__ void load_rows(const AttnArgs& a, const uint8_t* cach
                : "memory");
 }
 
-// Waits until at most n vector memory operations of this wave are in flight.
-template <int n>
+// Waits until at most kMost vector memory operations of this wave are in flight (63 where that is more than can be said).
+template <int kMost>
 __device__ __forceinline__ void wait_loads() {
-  static_assert(n >= 0 && n < 64, "6 bits");
+  constexpr int n = kMost < 63 ? kMost : 63;
   __builtin_amdgcn_s_waitcnt(0x0F70 | (n & 15) | ((n >> 4) << 14));
   asm volatile("" ::: "memory");
 }
 
-template <typename E, int D>
+// Waits until this wave's LDS reads have returned, before their place is loaded anew.
+__device__ __forceinline__ void wait_reads() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);
+  asm volatile("" ::: "memory");
+}
+
+// 32 rows of one wave. The last kQLds of the D / 16 query operands stay in LDS (`qs`, 1 KB each), the others in registers.
+template <typename E, int D, int kQLds>
 struct Wave {
   using L = Tile<E, D>;
-  Frag<E> q[D / 16];
+  static constexpr int kQRegs = D / 16 - kQLds;
+  static_assert(kQLds == 0 || sizeof(E) == 2, "16 bytes per lane");
+  Frag<E> q[kQRegs];
+  lds_u8* qs;
   f32x16 o[D / 32];
   float m, c, l;     // running maximum of the scores, the same times scale2 (log2 units), sum of the weights (this half-wave's keys)
   int32_t lo, hi;    // the keys this lane's row sees: lo <= j <= hi
@@ -243,17 +260,19 @@ struct Wave {
     const int32_t t = live ? r / a.group : 0, g = live ? r - t * a.group : 0;
     const uint8_t* src = a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + g) * D) * sizeof(E);
     const int h = lane >> 5;
+    const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
-      if (live)
-        q[x] = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
-      else
-        q[x].w = 0;
-    }
-    if (a.q_sign <= 0) {
-      const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) q[x].w = (q[x].w & keep) ^ flip;
+      Frag<E> f;
+      f.w = 0;
+      if (live) f = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
+      f.w = (f.w & keep) ^ flip;
+      if constexpr (kQLds == 0) {
+        q[x] = f;
+      } else {
+        if (x < kQRegs) q[x < kQRegs ? x : 0] = f;
+        else *(__attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16) = f.w;
+      }
     }
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
@@ -271,10 +290,11 @@ struct Wave {
     return sum;
   }
 
-  // Scores and weights of BN keys from kv0 on; `full`: every row of the wave sees them all.
-  template <int BN>
-  __device__ __forceinline__ void tile(const AttnArgs& a, const lds_u8* kt, const lds_u8* vt, int32_t kv0, bool full,
-                                       int lane) {
+  // Weights of BN keys from kv0 on; `full`: every row of the wave sees them all. `done` is called when the keys have
+  // been read.
+  template <int BN, typename Done>
+  __device__ __forceinline__ void scores(const AttnArgs& a, const lds_u8* kt, int32_t kv0, bool full, int lane,
+                                         Frag<E>* p, Done done) {
     const int h = lane >> 5;
     f32x16 s[BN / 32];
     {
@@ -294,10 +314,18 @@ struct Wave {
             const u32x4 w1 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64 + 16)));
             k.w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
           }
-          s[b] = mma(k, q[x], s[b]);
+          if constexpr (kQLds == 0) {
+            s[b] = mma(k, q[x], s[b]);
+          } else {
+            Frag<E> f;
+            if (x < kQRegs) f = q[x < kQRegs ? x : 0];
+            else f.w = *(const __attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16);
+            s[b] = mma(k, f, s[b]);
+          }
         }
       }
     }
+    done();
     if (!full) {
 #pragma unroll
       for (int b = 0; b < BN / 32; ++b)
@@ -324,7 +352,6 @@ struct Wave {
       c = c_new;
     }
     const float base = c == -INFINITY ? 0.0f : c;
-    Frag<E> p[BN / 16];
     float sum = 0.0f;
 #pragma unroll
     for (int b = 0; b < BN / 32; ++b)
@@ -339,6 +366,11 @@ struct Wave {
         p[2 * b + y] = pack(w, E{});
       }
     l += sum;
+  }
+
+  // Adds BN weighted values to the output.
+  template <int BN>
+  __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane) {
 #pragma unroll
     for (int x = 0; x < D / 32; ++x)
 #pragma unroll
@@ -463,14 +495,17 @@ __device__ __forceinline__ int64_t stretch_of(int64_t total, int grid, int least
 // every 4 D bytes (bf16) of keys and values, 16 flops per byte at 16 rows where
 // the card has some 250. Each wave streams tiles of 32 keys of its own
 // through its own LDS buffers without a barrier; the waves of a workgroup merge
-// at the end of a unit.
+// at the end of a unit. What counts is how many bytes are in flight: a
+// wave has two buffers of keys and two of values, and asks for the keys (values)
+// after next as soon as it has read those of the present tile.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32;
 
 template <typename E, int D>
 struct Narrow {
   static constexpr int kTileBytes = kNarrowKeys * D * int(sizeof(E));
-  // two buffers of keys and values per wave in 128 KB of LDS
+  // 128 KB of LDS per CU: two workgroups of four waves (D = 64, bf16), or one of as many waves as fit, four at most
   static constexpr int kWaves = kTileBytes <= 8192 ? 4 : 131072 / (4 * kTileBytes);
+  static constexpr int kGroups = 131072 / (kWaves * 4 * kTileBytes);
   static constexpr int kThreads = kWaves * 64;
 };
 
@@ -520,10 +555,10 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     total += sum;
   }
   total *= a.Hkv;
-  const int64_t stretch = stretch_of(total, a.grid, P::kWaves);
+  const int64_t stretch = stretch_of(total, a.narrow.grid, P::kWaves);
   int64_t pos = b * stretch;
   const int64_t end = min(pos + stretch, total);
-  if (tid == 0) a.joins[4 * b + 2] = 0;
+  if (tid == 0) a.narrow.joins[4 * b + 2] = 0;
   if (pos >= end) return;
   {
     int64_t before = 0;
@@ -543,7 +578,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   }
   int n = __builtin_amdgcn_readfirstlane(found_seq);
   int64_t rest = found_rest;   // position within the sequence's units
-  Wave<E, D> w;
+  Wave<E, D, 0> w;
   lds_u8* const mine = (lds_u8*)buf + wave * 4 * P::kTileBytes;
   while (pos < end && n < a.N) {
     const Seq s = seq_of(a, n);
@@ -561,31 +596,54 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
     w.start(a, s, hk, lane & 31, rows, lane);
 
-    auto load = [&](int32_t t, uint32_t to) {
+    auto load_keys = [&](int32_t t, uint32_t to) {
       const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < kLoads; ++i) load_rows<E, D, false>(a, a.kc, row, hk, kv0, last_page, i, to, lane);
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, i, to + P::kTileBytes, lane);
     };
+    auto load_values = [&](int32_t t, uint32_t to) {
+      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
+#pragma unroll 2
+      for (int i = 0; i < kLoads; ++i) load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, i, to, lane);
+    };
+    // mine: keys 0, keys 1, values 0, values 1
+    const uint32_t keys_at = uint32_t(uintptr_t(mine)), values_at = keys_at + 2 * P::kTileBytes;
+    constexpr int kW = P::kWaves;
     uint32_t half = 0;
     wait_loads<0>();   // no store of the unit before is counted below
-    if (t0 + wave < t1) load(t0 + wave, uint32_t(uintptr_t(mine)));
-    for (int32_t t = t0 + wave; t < t1; t += P::kWaves) {
-      if (t + P::kWaves < t1) {
-        load(t + P::kWaves, uint32_t(uintptr_t(mine)) + (half ^ 2 * P::kTileBytes));
-        wait_loads<(2 * kLoads < 63 ? 2 * kLoads : 63)>();   // all but the loads just issued
-      } else {
-        wait_loads<0>();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+      if (t0 + wave + i * kW < t1) {
+        load_keys(t0 + wave + i * kW, keys_at + i * P::kTileBytes);
+        load_values(t0 + wave + i * kW, values_at + i * P::kTileBytes);
       }
+    for (int32_t t = t0 + wave; t < t1; t += kW) {
+      const bool one = t + kW < t1, two = t + 2 * kW < t1;   // further tiles
       const int32_t kv0 = (x.lo + t) * kNarrowKeys;
       const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
-      if (!full && __any(any_odd<E, P::kTileBytes, 64>(mine + half + P::kTileBytes, lane))) {
-        w.template mark<kNarrowKeys>(mine + half + P::kTileBytes, kv0, lane);
-        clean<E, P::kTileBytes, 64>(mine + half + P::kTileBytes, lane);
+      Frag<E> p[kNarrowKeys / 16];
+      if (one) wait_loads<3 * kLoads>();  // behind these keys: these values, the next tile
+      else wait_loads<kLoads>();
+      w.template scores<kNarrowKeys>(a, mine + half, kv0, full, lane, p, [&] {
+        if (two) {
+          wait_reads();
+          load_keys(t + 2 * kW, keys_at + half);
+        }
+      });
+      if (two) wait_loads<3 * kLoads>();  // behind these values: the next tile, the keys after
+      else if (one) wait_loads<2 * kLoads>();
+      else wait_loads<0>();
+      lds_u8* const vt = mine + 2 * P::kTileBytes + half;
+      if (!full && __any(any_odd<E, P::kTileBytes, 64>(vt, lane))) {
+        w.template mark<kNarrowKeys>(vt, kv0, lane);
+        clean<E, P::kTileBytes, 64>(vt, lane);
       }
-      w.template tile<kNarrowKeys>(a, mine + half, mine + half + P::kTileBytes, kv0, full, lane);
-      half ^= 2 * P::kTileBytes;
+      w.template values<kNarrowKeys>(vt, p, lane);
+      if (two) {
+        wait_reads();
+        load_values(t + 2 * kW, values_at + half);
+      }
+      half ^= P::kTileBytes;
     }
 
     // The waves merge: maxima and sums first, then every thread sums some columns over the waves.
@@ -599,7 +657,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     }
     __syncthreads();
     const bool whole = t0 == 0 && t1 == tiles;
-    float* const part = a.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
+    float* const part = a.narrow.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
     // a half of the columns at a time: the merge buffer is one of the two stages
 #pragma unroll
     for (int x0 = 0; x0 < D / 32; x0 += (D / 32 + 1) / 2) {
@@ -652,10 +710,10 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     }
     if (tid == 0 && t0 > 0 && b * stretch == pos && pos - t0 >= (b - 1) * stretch) {
       // the first cut of this unit: it began in the stretch before
-      a.joins[4 * b] = n;
-      a.joins[4 * b + 1] = hk;
-      a.joins[4 * b + 3] = 0;
-      a.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+      a.narrow.joins[4 * b] = n;
+      a.narrow.joins[4 * b + 1] = hk;
+      a.narrow.joins[4 * b + 3] = 0;
+      a.narrow.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
     }
     pos += t1 - t0;
     rest = t1 < tiles ? rest + (t1 - t0) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * tiles : 0);
@@ -663,59 +721,87 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   }
 }
 
-// Merges the pieces of a unit that was cut, one row per D / 4 threads, in the order of the keys.
-template <typename E, int D, int kRows>
+// Merges the pieces of every unit that was cut, in the order of the keys. A
+// row takes D / 4 threads; the other threads of a workgroup take further rows
+// or, where there are many pieces, further pieces of the same row.
+template <typename E, int D, int kWideRows>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  constexpr int kLanes = D / 4, kSets = 256 / kLanes;   // threads of a row, pieces read side by side
+  constexpr int kLanes = D / 4, kSets = 256 / kLanes, kAhead = 4;
   __shared__ float4 acc_s[kSets][kLanes];
   __shared__ float l_s[kSets], c_s[kSets];
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int pieces = a.joins[4 * b + 2];
+  const bool wide = int(blockIdx.x) < a.wide.grid;
+  const Cuts& cuts = wide ? a.wide : a.narrow;
+  const int b = wide ? blockIdx.x : blockIdx.x - a.wide.grid, tid = threadIdx.x;
+  const int pieces = cuts.joins[4 * b + 2];
   if (pieces == 0) return;
-  const int n = a.joins[4 * b], hk = a.joins[4 * b + 1], r0 = a.joins[4 * b + 3];
+  const int n = cuts.joins[4 * b], hk = cuts.joins[4 * b + 1], r0 = cuts.joins[4 * b + 3];
   const Seq s = seq_of(a, n);
+  const int kRows = wide ? kWideRows : kNarrowRows;
+  const int64_t part_size = int64_t(kRows) * (D + 2);
+  const int rows = min(kRows, s.fresh * a.group - r0);
+  const bool share = pieces > kAhead;   // the sets share a row's pieces
   const int set = tid / kLanes, d = (tid % kLanes) * 4;
-  for (int q = blockIdx.y; q < kRows && r0 + q < s.fresh * a.group; q += gridDim.y) {
+  const int first = share ? set : 0, step = share ? kSets : 1, side = share ? 1 : kSets;
+  for (int q0 = blockIdx.y * side; q0 < rows; q0 += gridDim.y * side) {
+    const int q = q0 + (share ? 0 : set);
     float4 acc = {0, 0, 0, 0};
     float l = 0.0f, c = -INFINITY;
-    for (int i = set; i < pieces; i += kSets) {
-      const float* part = a.parts + int64_t(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)) * part_floats<D>(kRows);
-      const float pc = part[kRows * D + q], pl = part[kRows * (D + 1) + q];
-      const float4 z = *reinterpret_cast<const float4*>(part + q * D + d);
-      if (pc != -INFINITY) {
-        const float top = fmaxf(c, pc), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc - top);
-        acc.x = acc.x * f0 + z.x * f1;
-        acc.y = acc.y * f0 + z.y * f1;
-        acc.z = acc.z * f0 + z.z * f1;
-        acc.w = acc.w * f0 + z.w * f1;
-        l = l * f0 + pl * f1;
-        c = top;
-      }
-    }
-    acc_s[set][tid % kLanes] = acc;
-    if (d == 0) l_s[set] = l, c_s[set] = c;
-    __syncthreads();
-    if (set == 0) {
-      float top = -INFINITY;
-      for (int v = 0; v < kSets; ++v) top = fmaxf(top, c_s[v]);
-      float4 sum = {0, 0, 0, 0};
-      float ls = 0.0f;
-      for (int v = 0; v < kSets; ++v)
-        if (c_s[v] != -INFINITY) {
-          const float f = __builtin_amdgcn_exp2f(c_s[v] - top);
-          const float4 z = acc_s[v][tid];
-          sum.x += f * z.x;
-          sum.y += f * z.y;
-          sum.z += f * z.z;
-          sum.w += f * z.w;
-          ls += f * l_s[v];
+    for (int i0 = first; i0 < pieces && q < rows; i0 += kAhead * step) {
+      float pc[kAhead], pl[kAhead];
+      float4 z[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = i0 + k * step;
+        pc[k] = -INFINITY;
+        pl[k] = 0.0f;
+        z[k] = {0, 0, 0, 0};
+        if (i < pieces) {
+          const float* part = cuts.parts + int64_t(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)) * part_size;
+          pc[k] = part[kRows * D + q];
+          pl[k] = part[kRows * (D + 1) + q];
+          z[k] = *reinterpret_cast<const float4*>(part + q * D + d);
         }
-      const float inv = top == -INFINITY ? 0.0f : 1.0f / ls;
-      const int64_t r = out_row(a, s, hk, r0 + q);
-      store4<E>(a.o + (r * D + d) * sizeof(E), sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-      if (a.lse != nullptr && d == 0) a.lse[r] = top == -INFINITY ? -INFINITY : (top + log2f(ls)) * kLn2;
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (pc[k] != -INFINITY) {
+          const float top = fmaxf(c, pc[k]), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc[k] - top);
+          acc.x = acc.x * f0 + z[k].x * f1;
+          acc.y = acc.y * f0 + z[k].y * f1;
+          acc.z = acc.z * f0 + z[k].z * f1;
+          acc.w = acc.w * f0 + z[k].w * f1;
+          l = l * f0 + pl[k] * f1;
+          c = top;
+        }
     }
-    __syncthreads();
+    if (share) {
+      acc_s[set][tid % kLanes] = acc;
+      if (d == 0) l_s[set] = l, c_s[set] = c;
+      __syncthreads();
+      if (set == 0) {
+        c = -INFINITY;
+        for (int v = 0; v < kSets; ++v) c = fmaxf(c, c_s[v]);
+        acc = {0, 0, 0, 0};
+        l = 0.0f;
+        for (int v = 0; v < kSets; ++v)
+          if (c_s[v] != -INFINITY) {
+            const float f = __builtin_amdgcn_exp2f(c_s[v] - c);
+            const float4 y = acc_s[v][tid];
+            acc.x += f * y.x;
+            acc.y += f * y.y;
+            acc.z += f * y.z;
+            acc.w += f * y.w;
+            l += f * l_s[v];
+          }
+      }
+      __syncthreads();
+    }
+    if (q < rows && (!share || set == 0)) {
+      const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
+      const int64_t r = out_row(a, s, hk, r0 + q);
+      store4<E>(a.o + (r * D + d) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+      if (a.lse != nullptr && d == 0) a.lse[r] = c == -INFINITY ? -INFINITY : (c + log2f(l)) * kLn2;
+    }
   }
 }
 
@@ -726,10 +812,14 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
 // buffers while they work on the other; one barrier a tile.
 template <typename E, int D>
 struct Wide {
-  static constexpr int kWaves = D * int(sizeof(E)) <= 256 ? 8 : 4;
+  static constexpr bool kBf16 = sizeof(E) == 2;
+  // two waves per SIMD, so that one's softmax runs beside the other's products, where the registers allow: bf16 with
+  // D = 256 keeps half of its queries in LDS for that
+  static constexpr int kWaves = kBf16 || D == 64 ? 8 : 4;
   static constexpr int kThreads = kWaves * 64;
   static constexpr int kRows = kWaves * 32;
-  static constexpr int kKeys = D * int(sizeof(E)) <= 512 ? 64 : 32;
+  static constexpr int kKeys = D == 256 || (D == 128 && !kBf16) ? 32 : 64;
+  static constexpr int kQLds = kBf16 && D == 256 ? 8 : 0;
   static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
   static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
 };
@@ -748,7 +838,8 @@ __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
   int64_t count = 0, sum;
   for (int n0 = 0; n0 < a.N; n0 += kSchedThreads) {
     const int n = n0 + tid;
-    const int64_t v = n < a.N ? (int64_t(seq_of(a, n).fresh) * a.group + kRows - 1) / kRows : 0;
+    const int64_t rows = n < a.N ? int64_t(seq_of(a, n).fresh) * a.group : 0;
+    const int64_t v = rows > a.least_rows ? (rows + kRows - 1) / kRows : 0;
     const int64_t inc = count + block_scan<kSchedThreads>(v, part, sum);
     if (n < a.N) starts[n] = inc - v;
     count += sum;
@@ -785,16 +876,17 @@ template <typename E, int D>
 __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
   using P = Wide<E, D>;
   __shared__ __align__(1024) unsigned char buf[4 * P::kTileBytes];
+  __shared__ __align__(16) unsigned char queries[P::kQLds > 0 ? P::kWaves * P::kQLds * 1024 : 16];
   __shared__ int odd_waves[P::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
-  const int b = int(blockIdx.x % 8) * (a.grid / 8) + int(blockIdx.x / 8);
+  const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
   const int64_t count = a.sched[0], per_head = a.sched[1];
   const int64_t total = per_head * a.Hkv;
-  const int64_t stretch = stretch_of(total, a.grid, 1);
+  const int64_t stretch = stretch_of(total, a.wide.grid, 1);
   int64_t pos = b * stretch;
   const int64_t end = min(pos + stretch, total);
-  if (tid == 0) a.joins[4 * b + 2] = 0;
+  if (tid == 0) a.wide.joins[4 * b + 2] = 0;
   if (pos >= end) return;
   const int64_t* const before = a.sched + 2;
   const int64_t* const which = before + a.max_tiles;
@@ -814,8 +906,9 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     rt = __builtin_amdgcn_readfirstlane(int(lo));
     rest -= before[rt];
   }
-  Wave<E, D> w;
+  Wave<E, D, P::kQLds> w;
   lds_u8* const tiles_at = (lds_u8*)buf;
+  w.qs = (lds_u8*)queries + (P::kQLds > 0 ? wave * P::kQLds * 1024 : 0);
   while (pos < end) {
     const int64_t id = which[rt];
     const int n = __builtin_amdgcn_readfirstlane(int(id >> 32));
@@ -866,8 +959,11 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
           __syncthreads();
         }
       }
-      if (!none)
-        w.template tile<P::kKeys>(a, tiles_at + half, tiles_at + half + P::kTileBytes, kv0, full, lane);
+      if (!none) {
+        Frag<E> p[P::kKeys / 16];
+        w.template scores<P::kKeys>(a, tiles_at + half, kv0, full, lane, p, [] {});
+        w.template values<P::kKeys>(tiles_at + half + P::kTileBytes, p, lane);
+      }
       half ^= 2 * P::kTileBytes;
     }
     __syncthreads();   // before the next unit's loads
@@ -888,7 +984,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
         if (a.lse != nullptr && h == 0) a.lse[at] = w.c == -INFINITY ? -INFINITY : (w.c + log2f(l_all)) * kLn2;
       }
     } else {
-      float* const part = a.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(P::kRows);
+      float* const part = a.wide.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(P::kRows);
       const int q = wave * 32 + (lane & 31);
       if (r < rows) {
 #pragma unroll
@@ -904,10 +1000,10 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
         }
       }
       if (tid == 0 && t0 > 0 && pos == b * stretch && pos - t0 >= (b - 1) * stretch) {
-        a.joins[4 * b] = n;
-        a.joins[4 * b + 1] = hk;
-        a.joins[4 * b + 3] = r0;
-        a.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+        a.wide.joins[4 * b] = n;
+        a.wide.joins[4 * b + 1] = hk;
+        a.wide.joins[4 * b + 3] = r0;
+        a.wide.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
       }
     }
     pos += t1 - t0;
@@ -935,39 +1031,52 @@ int64_t most_rows(const rglru_paged_shape_t& s) {
   return longest * (s.q_heads / s.kv_heads);
 }
 
+// A call whose sequences may all have at most kNarrowRows rows runs the narrow
+// kernel alone; any other one the wide kernel, and the narrow kernel before it for the sequences of few
+// rows among more than kFewSeqs. With few sequences the wide kernel takes them all: the launch would cost more
+// than the rows it leaves idle.
+constexpr int kFewSeqs = 4;
+
 struct Plan {
-  bool narrow;
-  int grid;             // workgroups, a multiple of 8
-  int64_t max_tiles;    // row tiles at most (wide)
-  size_t joins, parts, bytes;  // offsets and size of the workspace
+  bool narrow, wide;
+  int narrow_grid, wide_grid;  // workgroups; of the wide kernel a multiple of 8
+  int64_t max_tiles;           // row tiles of the wide kernel at most
+  size_t narrow_joins, narrow_parts, wide_joins, wide_parts, sched, bytes;  // offsets and size of the workspace
 };
 
 template <typename E, int D>
 Plan plan_of(const rglru_paged_shape_t& s) {
-  Plan p;
-  p.narrow = most_rows(s) <= kNarrowRows;
+  using W = Wide<E, D>;
+  Plan p = {};
+  p.wide = most_rows(s) > kNarrowRows;
+  p.narrow = !p.wide || s.n_seqs > kFewSeqs;
   const int64_t group = s.q_heads / s.kv_heads;
   const int64_t keys = int64_t(s.max_pages) * s.page_size;
   const int64_t seqs = s.n_seqs < s.n_tokens ? s.n_seqs : s.n_tokens;
-  int64_t units, tiles;  // upper bounds on units and on the tiles of one
+  size_t at = 0;
+  auto take = [&at](size_t bytes) {
+    const size_t start = at;
+    at += round_up(bytes, 256);
+    return start;
+  };
+  // no more workgroups than there can be tiles
+  auto grid_of = [](int64_t most, int64_t units, int64_t tiles) {
+    return int(units >= most || tiles >= most || units * tiles >= most ? most : units * tiles > 0 ? units * tiles : 1);
+  };
   if (p.narrow) {
-    units = seqs * s.kv_heads;
-    tiles = ceil_div(ceil_div(keys, kNarrowKeys), Narrow<E, D>::kWaves);
-    p.max_tiles = 0;
-  } else {
-    p.max_tiles = ceil_div(s.n_tokens * group, Wide<E, D>::kRows) + seqs;
-    units = p.max_tiles * s.kv_heads;
-    tiles = ceil_div(keys, Wide<E, D>::kKeys);
+    using P = Narrow<E, D>;
+    p.narrow_grid = grid_of(256 * P::kGroups, seqs * s.kv_heads, ceil_div(ceil_div(keys, kNarrowKeys), P::kWaves));
+    p.narrow_joins = take(size_t(p.narrow_grid) * 16);
+    p.narrow_parts = take(size_t(p.narrow_grid) * 2 * part_floats<D>(kNarrowRows) * 4);
   }
-  const int64_t most = 256;
-  int64_t grid = units >= most || tiles >= most ? most : units * tiles;
-  if (grid > most) grid = most;
-  p.grid = int((grid + 7) / 8 * 8);
-  const int rows = p.narrow ? kNarrowRows : Wide<E, D>::kRows;
-  const size_t sched = p.narrow ? 0 : round_up(size_t(2 + 2 * p.max_tiles + s.n_seqs) * 8, 256);
-  p.joins = sched;
-  p.parts = p.joins + round_up(size_t(p.grid) * 16, 256);
-  p.bytes = p.parts + size_t(p.grid) * 2 * part_floats<D>(rows) * 4;
+  if (p.wide) {
+    p.max_tiles = ceil_div(s.n_tokens * group, W::kRows) + seqs;
+    p.wide_grid = (grid_of(256, p.max_tiles * s.kv_heads, ceil_div(keys, W::kKeys)) + 7) / 8 * 8;
+    p.sched = take(size_t(2 + 2 * p.max_tiles + s.n_seqs) * 8);
+    p.wide_joins = take(size_t(p.wide_grid) * 16);
+    p.wide_parts = take(size_t(p.wide_grid) * 2 * part_floats<D>(W::kRows) * 4);
+  }
+  p.bytes = at;
   return p;
 }
 
@@ -978,22 +1087,22 @@ size_t bytes_of(const rglru_paged_shape_t& s) {
 
 template <typename E, int D>
 void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStream_t st) {
+  using W = Wide<E, D>;
   const Plan p = plan_of<E, D>(s);
-  a.sched = reinterpret_cast<int64_t*>(workspace);
-  a.joins = reinterpret_cast<int32_t*>(workspace + p.joins);
-  a.parts = reinterpret_cast<float*>(workspace + p.parts);
-  a.grid = p.grid;
+  a.narrow = {reinterpret_cast<int32_t*>(workspace + p.narrow_joins), reinterpret_cast<float*>(workspace + p.narrow_parts),
+              p.narrow_grid};
+  a.wide = {reinterpret_cast<int32_t*>(workspace + p.wide_joins), reinterpret_cast<float*>(workspace + p.wide_parts),
+            p.wide_grid};
+  a.sched = reinterpret_cast<int64_t*>(workspace + p.sched);
   a.max_tiles = int32_t(p.max_tiles);
-  const int64_t most = most_rows(s);
-  if (p.narrow) {
-    narrow_kernel<E, D><<<unsigned(p.grid), Narrow<E, D>::kThreads, 0, st>>>(a);
-    join_kernel<E, D, kNarrowRows><<<dim3(unsigned(p.grid), unsigned(most)), 256, 0, st>>>(a);
-  } else {
-    using P = Wide<E, D>;
-    sched_kernel<P::kRows, P::kKeys><<<1, kSchedThreads, 0, st>>>(a);
-    wide_kernel<E, D><<<unsigned(p.grid), P::kThreads, 0, st>>>(a);
-    join_kernel<E, D, P::kRows><<<dim3(unsigned(p.grid), P::kRows / 8), 256, 0, st>>>(a);
+  a.least_rows = p.narrow ? kNarrowRows : 0;
+  if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid), Narrow<E, D>::kThreads, 0, st>>>(a);
+  if (p.wide) {
+    sched_kernel<W::kRows, W::kKeys><<<1, kSchedThreads, 0, st>>>(a);
+    wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
+  const unsigned rows = p.wide ? W::kRows * D / 1024 : unsigned(most_rows(s));
+  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), rows), 256, 0, st>>>(a);
 }
 
 // Calls f<E, D>(...) for the shape's type and head width.
