@@ -55,13 +55,11 @@ template <typename E>
 struct Frag;
 template <>
 struct Frag<uint16_t> {
-  static constexpr int kWords = 4;
   static constexpr uint32_t kSigns = 0x80008000u;
   u32x4 w;
 };
 template <>
 struct Frag<float> {
-  static constexpr int kWords = 8;
   static constexpr uint32_t kSigns = 0x80000000u;
   u32x8 w;
 };
@@ -208,25 +206,44 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const Seq& s, int32_t
   return x;
 }
 
-// Loads rows kv0 + i * kLoadRows .. of a tile of keys or values straight into LDS; `i` counts the tile's loads. All rows
-// of a load are in one page: kLoadRows is at most 8, the smallest page.
-template <typename E, int D, bool kValues>
-__device__ __forceinline__ void load_rows(const AttnArgs& a, const uint8_t* cache, const_i32* row, int hk,
-                                          int32_t kv0, int32_t last_page, int i, uint32_t tile, int lane) {
-  using L = Tile<E, D>;
-  const int32_t j = kv0 + i * L::kLoadRows;
-  const int32_t page = min(max(row[min(j >> a.lps, last_page)], 0), a.n_pages - 1);
-  const int64_t at = ((int64_t(page) * a.Hkv + hk) << a.lps) + (j & ((1 << a.lps) - 1));
-  const uint8_t* base = cache + at * L::kRowBytes;
-  const int r = lane / L::kCols, c = lane % L::kCols;
-  const int lane_swz = kValues ? L::swz_v(r) : L::swz_k(r);
-  const int load_swz = kValues ? L::swz_v(i * L::kLoadRows) : L::swz_k(i * L::kLoadRows);
-  const uint32_t off = uint32_t(((c ^ lane_swz) * 16 + r * L::kRowBytes) ^ (load_swz * 16));
-  // 64 lanes x 16 bytes to LDS at m0. Written out because the compiler, which cannot tell the buffers apart, would wait
-  // for every load in flight before each transposing LDS read. It has no output register; its arrival is waited for by
-  // wait_loads, which every path passes before the tile is read.
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(tile + i * 1024), "v"(off), "s"(base)
+// Eight rows of the cache lie in one page (the smallest page), so they are one
+// piece of memory. seg_page looks up the page of rows j .. j + 7 of a sequence,
+// seg_offset gives their place, in bytes.
+constexpr int kSeg = 8;
+
+__device__ __forceinline__ int32_t seg_page(const AttnArgs& a, const_i32* row, int32_t last_page, int32_t j) {
+  return row[min(j >> a.lps, last_page)];
+}
+template <typename E, int D>
+__device__ __forceinline__ int64_t seg_offset(const AttnArgs& a, int32_t page, int hk, int32_t j) {
+  const int64_t p = min(max(page, 0), a.n_pages - 1);
+  return (((p * a.Hkv + hk) << a.lps) + (j & ((1 << a.lps) - 1))) * Tile<E, D>::kRowBytes;
+}
+
+// 64 lanes x 16 bytes from base + off + kAt to LDS at `to` + kAt. Written out
+// because the compiler, which cannot tell the buffers apart, would wait for every
+// load in flight before each transposing LDS read. It has no output register; its arrival
+// is waited for by wait_loads, which every path passes before the tile is read.
+template <int kAt>
+__device__ __forceinline__ void load_lds(uint32_t to, uint32_t off, const uint8_t* base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 offset:%3" ::"s"(to), "v"(off), "s"(base),
+               "n"(kAt)
                : "memory");
+}
+
+// Loads kCount KB of consecutive rows, from row r of a tile on, straight into LDS (`to`: where row r goes).
+template <typename E, int D, bool kValues, int kCount, int kFrom = 0>
+__device__ __forceinline__ void load_rows(const uint8_t* base, int r, uint32_t to, int lane) {
+  using L = Tile<E, D>;
+  if constexpr (kFrom < kCount) {
+    const int x = lane / L::kCols, c = lane % L::kCols;
+    const int lane_swz = kValues ? L::swz_v(x) : L::swz_k(x);
+    const int row = r + kFrom * L::kLoadRows;
+    const int load_swz = kValues ? L::swz_v(row) : L::swz_k(row);
+    const uint32_t off = uint32_t((((c ^ lane_swz) * 16) ^ (load_swz * 16)) + x * L::kRowBytes);
+    load_lds<(kFrom % 4) * 1024>(to + (kFrom & ~3) * 1024, off, base + (kFrom & ~3) * 1024);
+    load_rows<E, D, kValues, kCount, kFrom + 1>(base, r, to, lane);
+  }
 }
 
 // Waits until at most kMost vector memory operations of this wave are in flight (63 where that is more than can be said).
@@ -341,15 +358,17 @@ struct Wave {
 #pragma unroll
       for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
     top = half_max(top);
-    if (__any(top * a.scale2 > c + kSlack)) {
-      const float m_new = fmaxf(m, top), c_new = m_new * a.scale2;
+    // the wave branches together, each row decides for itself: what other rows see must not change its bits
+    const bool grow = top * a.scale2 > c + kSlack;
+    if (__any(grow)) {
+      const float m_new = grow ? fmaxf(m, top) : m, c_new = m_new * a.scale2;
       // never 0, so that an infinite output stays one (the smallest float leaves nothing else behind)
-      const float keep = c == -INFINITY ? 1.0f : fmaxf(__builtin_amdgcn_exp2f(c - c_new), FLT_MIN);
+      const float keep = grow && c != -INFINITY ? fmaxf(__builtin_amdgcn_exp2f(c - c_new), FLT_MIN) : 1.0f;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) o[x] *= keep;
       l *= keep;
       m = m_new;
-      c = c_new;
+      c = grow ? c_new : c;
     }
     const float base = c == -INFINITY ? 0.0f : c;
     float sum = 0.0f;
@@ -436,8 +455,8 @@ template <typename E, int kTileBytes, int kThreads>
 __device__ __forceinline__ bool any_odd(const lds_u8* vt, int thread) {
   uint32_t odd = 0;
 #pragma unroll
-  for (int i = thread * 16; i < kTileBytes; i += kThreads * 16) {
-    const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i);
+  for (int i = 0; i < kTileBytes; i += kThreads * 16) {
+    const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i + thread * 16);
 #pragma unroll
     for (int j = 0; j < 4; ++j) odd |= odd_bits(w[j], E{});
   }
@@ -479,12 +498,12 @@ constexpr int part_floats(int rows) {
 }
 
 // The share of the work of workgroup b: the units (sequence, key head, row
-// tile) stand in one line, each as long as its tiles of keys, and every
-// workgroup takes an equal stretch of that line, at least `least` tiles. A unit
+// tile) stand in one line, each as long as its tiles of keys and a fixed part for
+// starting and ending it (kOver tiles' worth), and every workgroup takes an equal stretch of that line. A unit
 // that lies in one stretch is finished there; the pieces of one that is cut
 // go to `parts` (slot 0: the unit began in an earlier stretch, slot 1: it began
 // here) and the join after the cut merges them in order, so the bits do not
-// depend on timing.
+// depend on timing. A cut within the fixed part moves to the unit's start.
 __device__ __forceinline__ int64_t stretch_of(int64_t total, int grid, int least) {
   return max((total + grid - 1) / grid, int64_t(least));
 }
@@ -498,7 +517,7 @@ __device__ __forceinline__ int64_t stretch_of(int64_t total, int grid, int least
 // at the end of a unit. What counts is how many bytes are in flight: a
 // wave has two buffers of keys and two of values, and asks for the keys (values)
 // after next as soon as it has read those of the present tile.
-constexpr int kNarrowRows = 32, kNarrowKeys = 32;
+constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
 
 template <typename E, int D>
 struct Narrow {
@@ -527,11 +546,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t&
   return v;
 }
 
-__device__ __forceinline__ int32_t narrow_tiles(const AttnArgs& a, int n) {
+// Length of a unit of sequence n in the line.
+__device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, int n) {
   const Seq s = seq_of(a, n);
   if (s.fresh == 0 || int64_t(s.fresh) * a.group > kNarrowRows) return 0;
   const Span x = span_of<kNarrowKeys>(a, s, 0, s.fresh * a.group - 1);
-  return x.hi - x.lo;
+  return x.hi - x.lo + kNarrowOver;
 }
 
 template <typename E, int D>
@@ -551,11 +571,11 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
     const int n = n0 + tid;
     int64_t sum;
-    block_scan<P::kThreads>(n < a.N ? narrow_tiles(a, n) : 0, scan_part, sum);
+    block_scan<P::kThreads>(n < a.N ? narrow_size(a, n) : 0, scan_part, sum);
     total += sum;
   }
   total *= a.Hkv;
-  const int64_t stretch = stretch_of(total, a.narrow.grid, P::kWaves);
+  const int64_t stretch = stretch_of(total, a.narrow.grid, P::kWaves + kNarrowOver);
   int64_t pos = b * stretch;
   const int64_t end = min(pos + stretch, total);
   if (tid == 0) a.narrow.joins[4 * b + 2] = 0;
@@ -564,7 +584,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     int64_t before = 0;
     for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
       const int n = n0 + tid;
-      const int64_t t = n < a.N ? int64_t(narrow_tiles(a, n)) * a.Hkv : 0;
+      const int64_t t = n < a.N ? int64_t(narrow_size(a, n)) * a.Hkv : 0;
       int64_t sum;
       const int64_t inc = before + block_scan<P::kThreads>(t, scan_part, sum);
       if (pos >= inc - t && pos < inc) {
@@ -588,34 +608,50 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       continue;
     }
     const Span x = span_of<kNarrowKeys>(a, s, 0, rows - 1);
-    const int32_t tiles = x.hi - x.lo;
-    const int hk = __builtin_amdgcn_readfirstlane(int(rest / tiles));
-    const int32_t t0 = int32_t(rest - int64_t(hk) * tiles);
-    const int32_t t1 = int32_t(min(int64_t(tiles), t0 + (end - pos)));
+    const int32_t tiles = x.hi - x.lo, size = tiles + kNarrowOver;
+    const int hk = __builtin_amdgcn_readfirstlane(int(rest / size));
+    const int32_t in = int32_t(rest - int64_t(hk) * size);   // where this stretch enters the unit and leaves it
+    const int32_t out = int32_t(min(int64_t(size), in + (end - pos)));
+    if (out <= kNarrowOver) break;   // left to the next workgroup
+    const int32_t t0 = max(in - kNarrowOver, 0), t1 = out - kNarrowOver;
     const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
     w.start(a, s, hk, lane & 31, rows, lane);
 
+    constexpr int kSegs = kNarrowKeys / kSeg, kSegLoads = kLoads / kSegs;
+    // the pages of the tile to load next are looked up one tile ahead
+    int32_t pages[kSegs];
+    int64_t at[kSegs];
+    auto look_up = [&](int32_t t) {
+      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i) pages[i] = seg_page(a, row, last_page, kv0 + i * kSeg);
+    };
     auto load_keys = [&](int32_t t, uint32_t to) {
       const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
-#pragma unroll 2
-      for (int i = 0; i < kLoads; ++i) load_rows<E, D, false>(a, a.kc, row, hk, kv0, last_page, i, to, lane);
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i) {
+        at[i] = seg_offset<E, D>(a, pages[i], hk, kv0 + i * kSeg);
+        load_rows<E, D, false, kSegLoads>(a.kc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
+      }
     };
-    auto load_values = [&](int32_t t, uint32_t to) {
-      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
-#pragma unroll 2
-      for (int i = 0; i < kLoads; ++i) load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, i, to, lane);
+    auto load_values = [&](uint32_t to) {
+#pragma unroll
+      for (int i = 0; i < kSegs; ++i)
+        load_rows<E, D, true, kSegLoads>(a.vc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
     };
     // mine: keys 0, keys 1, values 0, values 1
     const uint32_t keys_at = uint32_t(uintptr_t(mine)), values_at = keys_at + 2 * P::kTileBytes;
     constexpr int kW = P::kWaves;
     uint32_t half = 0;
+    look_up(t0 + wave);
     wait_loads<0>();   // no store of the unit before is counted below
 #pragma unroll 1
     for (int i = 0; i < 2; ++i)
       if (t0 + wave + i * kW < t1) {
         load_keys(t0 + wave + i * kW, keys_at + i * P::kTileBytes);
-        load_values(t0 + wave + i * kW, values_at + i * P::kTileBytes);
+        load_values(values_at + i * P::kTileBytes);
+        look_up(t0 + wave + (i + 1) * kW);
       }
     for (int32_t t = t0 + wave; t < t1; t += kW) {
       const bool one = t + kW < t1, two = t + 2 * kW < t1;   // further tiles
@@ -641,7 +677,8 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       w.template values<kNarrowKeys>(vt, p, lane);
       if (two) {
         wait_reads();
-        load_values(t + 2 * kW, values_at + half);
+        load_values(values_at + half);
+        look_up(t + 3 * kW);
       }
       half ^= P::kTileBytes;
     }
@@ -708,16 +745,16 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       }
       __syncthreads();
     }
-    if (tid == 0 && t0 > 0 && b * stretch == pos && pos - t0 >= (b - 1) * stretch) {
-      // the first cut of this unit: it began in the stretch before
+    if (tid == 0 && t0 > 0 && (b - 1) * stretch <= pos - in + kNarrowOver) {
+      // the first cut of this unit: the one before is not within it
       a.narrow.joins[4 * b] = n;
       a.narrow.joins[4 * b + 1] = hk;
       a.narrow.joins[4 * b + 3] = 0;
-      a.narrow.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+      a.narrow.joins[4 * b + 2] = 1 + int32_t((size - in + stretch - 1) / stretch);
     }
-    pos += t1 - t0;
-    rest = t1 < tiles ? rest + (t1 - t0) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * tiles : 0);
-    if (t1 == tiles && hk + 1 == a.Hkv) ++n;
+    pos += out - in;
+    rest = out < size ? rest + (out - in) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * size : 0);
+    if (out == size && hk + 1 == a.Hkv) ++n;
   }
 }
 
@@ -726,7 +763,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
 // or, where there are many pieces, further pieces of the same row.
 template <typename E, int D, int kWideRows>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  constexpr int kLanes = D / 4, kSets = 256 / kLanes, kAhead = 4;
+  constexpr int kLanes = D / 4, kSets = 256 / kLanes, kAhead = 4, kShare = 16;
   __shared__ float4 acc_s[kSets][kLanes];
   __shared__ float l_s[kSets], c_s[kSets];
   const bool wide = int(blockIdx.x) < a.wide.grid;
@@ -739,69 +776,61 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   const int kRows = wide ? kWideRows : kNarrowRows;
   const int64_t part_size = int64_t(kRows) * (D + 2);
   const int rows = min(kRows, s.fresh * a.group - r0);
-  const bool share = pieces > kAhead;   // the sets share a row's pieces
+  const bool share = pieces > kShare;   // the sets share a row's pieces
   const int set = tid / kLanes, d = (tid % kLanes) * 4;
-  const int first = share ? set : 0, step = share ? kSets : 1, side = share ? 1 : kSets;
+  auto write = [&](int q, float c, float l, const float4& acc) {
+    const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
+    const int64_t r = out_row(a, s, hk, r0 + q);
+    store4<E>(a.o + (r * D + d) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (a.lse != nullptr && d == 0) a.lse[r] = c == -INFINITY ? -INFINITY : (c + log2f(l)) * kLn2;
+  };
+  auto fetch = [&](int i, int q, float& pc, float& pl, float4& z) {
+    const float* part = cuts.parts + int64_t(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)) * part_size;
+    pc = part[kRows * D + q];
+    pl = part[kRows * (D + 1) + q];
+    z = *reinterpret_cast<const float4*>(part + q * D + d);
+  };
+  auto merge = [](float& c, float& l, float4& acc, float pc, float pl, const float4& z) {
+    if (pc == -INFINITY) return;
+    const float top = fmaxf(c, pc), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc - top);
+    acc.x = acc.x * f0 + z.x * f1;
+    acc.y = acc.y * f0 + z.y * f1;
+    acc.z = acc.z * f0 + z.z * f1;
+    acc.w = acc.w * f0 + z.w * f1;
+    l = l * f0 + pl * f1;
+    c = top;
+  };
+  const int step = share ? kSets : 1, side = share ? 1 : kSets;
   for (int q0 = blockIdx.y * side; q0 < rows; q0 += gridDim.y * side) {
-    const int q = q0 + (share ? 0 : set);
+    const int q = min(q0 + (share ? 0 : set), rows - 1);
     float4 acc = {0, 0, 0, 0};
     float l = 0.0f, c = -INFINITY;
-    for (int i0 = first; i0 < pieces && q < rows; i0 += kAhead * step) {
+    for (int i0 = share ? set : 0; i0 < pieces; i0 += kAhead * step) {
       float pc[kAhead], pl[kAhead];
       float4 z[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
         const int i = i0 + k * step;
-        pc[k] = -INFINITY;
-        pl[k] = 0.0f;
-        z[k] = {0, 0, 0, 0};
-        if (i < pieces) {
-          const float* part = cuts.parts + int64_t(i == 0 ? 2 * (b - 1) + 1 : 2 * (b + i - 1)) * part_size;
-          pc[k] = part[kRows * D + q];
-          pl[k] = part[kRows * (D + 1) + q];
-          z[k] = *reinterpret_cast<const float4*>(part + q * D + d);
-        }
+        fetch(min(i, pieces - 1), q, pc[k], pl[k], z[k]);
+        if (i >= pieces) pc[k] = -INFINITY;
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (pc[k] != -INFINITY) {
-          const float top = fmaxf(c, pc[k]), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc[k] - top);
-          acc.x = acc.x * f0 + z[k].x * f1;
-          acc.y = acc.y * f0 + z[k].y * f1;
-          acc.z = acc.z * f0 + z[k].z * f1;
-          acc.w = acc.w * f0 + z[k].w * f1;
-          l = l * f0 + pl[k] * f1;
-          c = top;
-        }
+      for (int k = 0; k < kAhead; ++k) merge(c, l, acc, pc[k], pl[k], z[k]);
     }
-    if (share) {
-      acc_s[set][tid % kLanes] = acc;
-      if (d == 0) l_s[set] = l, c_s[set] = c;
-      __syncthreads();
-      if (set == 0) {
-        c = -INFINITY;
-        for (int v = 0; v < kSets; ++v) c = fmaxf(c, c_s[v]);
-        acc = {0, 0, 0, 0};
-        l = 0.0f;
-        for (int v = 0; v < kSets; ++v)
-          if (c_s[v] != -INFINITY) {
-            const float f = __builtin_amdgcn_exp2f(c_s[v] - c);
-            const float4 y = acc_s[v][tid];
-            acc.x += f * y.x;
-            acc.y += f * y.y;
-            acc.z += f * y.z;
-            acc.w += f * y.w;
-            l += f * l_s[v];
-          }
-      }
-      __syncthreads();
+    if (!share) {
+      if (q0 + set < rows) write(q, c, l, acc);
+      continue;
     }
-    if (q < rows && (!share || set == 0)) {
-      const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
-      const int64_t r = out_row(a, s, hk, r0 + q);
-      store4<E>(a.o + (r * D + d) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-      if (a.lse != nullptr && d == 0) a.lse[r] = c == -INFINITY ? -INFINITY : (c + log2f(l)) * kLn2;
+    acc_s[set][tid % kLanes] = acc;
+    if (d == 0) l_s[set] = l, c_s[set] = c;
+    __syncthreads();
+    if (set == 0) {
+      c = -INFINITY, l = 0.0f;
+      acc = {0, 0, 0, 0};
+      for (int v = 0; v < kSets; ++v) merge(c, l, acc, c_s[v], l_s[v], acc_s[v][tid]);
+      write(q, c, l, acc);
     }
+    __syncthreads();
   }
 }
 
@@ -824,8 +853,11 @@ struct Wide {
   static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
 };
 
-// The row tiles of all sequences: sched[0] their number, sched[1] the tiles of
-// keys of one key head, then for each the tiles before it and (sequence << 32 | row tile).
+constexpr int kWideOver = 2;
+constexpr int kSlackPart = 16;  // a cut moves by up to a sixteenth of a stretch
+
+// The row tiles of all sequences: sched[0] their number, sched[1] the length
+// of one key head's units, then for each tile the length before it and (sequence << 32 | row tile).
 constexpr int kSchedThreads = 1024;
 
 template <int kRows, int kKeys>
@@ -859,7 +891,7 @@ __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
       const Seq s = seq_of(a, lo);
       const int32_t r0 = int32_t(t - starts[lo]) * kRows;
       const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
-      v = x.hi - x.lo;
+      v = x.hi - x.lo + kWideOver;
       which[t] = int64_t(lo) << 32 | (t - starts[lo]);
     }
     const int64_t inc = total + block_scan<kSchedThreads>(v, part, sum);
@@ -883,29 +915,49 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
   const int64_t count = a.sched[0], per_head = a.sched[1];
   const int64_t total = per_head * a.Hkv;
-  const int64_t stretch = stretch_of(total, a.wide.grid, 1);
-  int64_t pos = b * stretch;
-  const int64_t end = min(pos + stretch, total);
+  const int64_t stretch = stretch_of(total, a.wide.grid, 1 + kWideOver);
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
-  if (pos >= end) return;
   const int64_t* const before = a.sched + 2;
   const int64_t* const which = before + a.max_tiles;
-  int hk = __builtin_amdgcn_readfirstlane(int(pos / per_head));
-  int64_t rest = pos - hk * per_head;
-  int rt;
-  {
-    // the last row tile that starts at or before `rest`, 64 probes at a time
+  // The unit that holds position `at`: key head, row tile, start.
+  auto find = [&](int64_t at, int& head, int& tile, int64_t& start, int64_t& size) {
+    head = __builtin_amdgcn_readfirstlane(int(at / per_head));
+    const int64_t in = at - head * per_head;
+    // the last row tile that starts at or before `in`, 64 probes at a time
     int64_t lo = 0, len = count;
     while (len > 1) {
-      const int64_t step = (len + 63) / 64, at = lo + lane * step;
-      const int hits = __popcll(__ballot(at < lo + len && before[min(at, count - 1)] <= rest));
+      const int64_t step = (len + 63) / 64, probe = lo + lane * step;
+      const int hits = __popcll(__ballot(probe < lo + len && before[min(probe, count - 1)] <= in));
       const int64_t next = lo + max(hits - 1, 0) * step;
       len = min(step, lo + len - next);
       lo = next;
     }
-    rt = __builtin_amdgcn_readfirstlane(int(lo));
-    rest -= before[rt];
+    tile = __builtin_amdgcn_readfirstlane(int(lo));
+    start = before[tile] + head * per_head;
+    size = (tile + 1 < count ? before[tile + 1] : per_head) - before[tile];
+  };
+  // A cut costs a write and a read of a whole output tile, so one that falls near an end of a unit moves there (and one
+  // in its fixed part always).
+  const int64_t slack = max(stretch / kSlackPart, int64_t(kWideOver));
+  auto snap = [&](int64_t at, int64_t start, int64_t size) {
+    const int64_t off = at - start;
+    return off <= size - off ? (off <= slack ? start : at) : (size - off <= slack ? start + size : at);
+  };
+  int hk, rt, other_hk, other_rt;
+  int64_t start, length, pos = total, end = total;
+  if ((b + 1) * stretch < total) {
+    find((b + 1) * stretch, other_hk, other_rt, start, length);
+    end = snap((b + 1) * stretch, start, length);
   }
+  if (b * stretch >= total) return;
+  find(b * stretch, hk, rt, start, length);
+  pos = snap(b * stretch, start, length);
+  if (pos >= end) return;
+  if (pos == start + length) {
+    start = pos;
+    if (++rt >= count) rt = 0, ++hk;
+  }
+  int64_t rest = pos - start;
   Wave<E, D, P::kQLds> w;
   lds_u8* const tiles_at = (lds_u8*)buf;
   w.qs = (lds_u8*)queries + (P::kQLds > 0 ? wave * P::kQLds * 1024 : 0);
@@ -916,9 +968,10 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     const int32_t rows = s.fresh * a.group;
     const int32_t r0 = __builtin_amdgcn_readfirstlane(int(id & 0xFFFFFFFF)) * P::kRows;
     const Span x = span_of<P::kKeys>(a, s, r0, max(min(r0 + P::kRows, rows) - 1, r0));
-    const int32_t tiles = x.hi - x.lo;
-    const int32_t t0 = __builtin_amdgcn_readfirstlane(int32_t(rest));
-    const int32_t t1 = __builtin_amdgcn_readfirstlane(int32_t(min(int64_t(tiles), t0 + (end - pos))));
+    const int32_t tiles = x.hi - x.lo, size = tiles + kWideOver;
+    const int32_t in = __builtin_amdgcn_readfirstlane(int32_t(rest));   // where this stretch enters the unit and leaves it
+    const int32_t out = __builtin_amdgcn_readfirstlane(int32_t(min(int64_t(size), in + (end - pos))));
+    const int32_t t0 = max(in - kWideOver, 0), t1 = max(out - kWideOver, 0);
     const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
     const int32_t w0 = r0 + wave * 32;   // this wave's rows
@@ -926,14 +979,17 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     const Span mine = span_of<P::kKeys>(a, s, min(w0, rows - 1), min(w0 + 31, rows - 1));
     w.start(a, s, hk, w0 + (lane & 31), rows, lane);
 
+    // this wave's share of a tile: rows mine_at .., all in one page, looked up one tile ahead
+    constexpr int kMine = P::kKeys / P::kWaves;
+    static_assert(kMine <= kSeg && kSeg % kMine == 0, "one page");
+    const int mine_at = wave * kMine;
+    int32_t page = seg_page(a, row, last_page, (x.lo + t0) * P::kKeys + mine_at);
     auto load = [&](int32_t t, uint32_t to) {
-      const int32_t kv0 = (x.lo + t) * P::kKeys;
-#pragma unroll
-      for (int i = 0; i < P::kLoads; ++i)
-        load_rows<E, D, false>(a, a.kc, row, hk, kv0, last_page, wave * P::kLoads + i, to, lane);
-#pragma unroll
-      for (int i = 0; i < P::kLoads; ++i)
-        load_rows<E, D, true>(a, a.vc, row, hk, kv0, last_page, wave * P::kLoads + i, to + P::kTileBytes, lane);
+      const int32_t j = (x.lo + t) * P::kKeys + mine_at;
+      const int64_t at = seg_offset<E, D>(a, page, hk, j);
+      load_rows<E, D, false, P::kLoads>(a.kc + at, mine_at, to + mine_at * Tile<E, D>::kRowBytes, lane);
+      load_rows<E, D, true, P::kLoads>(a.vc + at, mine_at, to + P::kTileBytes + mine_at * Tile<E, D>::kRowBytes, lane);
+      page = seg_page(a, row, last_page, j + P::kKeys);
     };
     uint32_t half = 0;
     load(t0, uint32_t(uintptr_t(tiles_at)));
@@ -999,14 +1055,15 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
           part[P::kRows * (D + 1) + q] = l_all;
         }
       }
-      if (tid == 0 && t0 > 0 && pos == b * stretch && pos - t0 >= (b - 1) * stretch) {
+      // the first cut of this unit: the one before is not within it (or has moved to its start)
+      if (tid == 0 && t0 > 0 && (b - 1) * stretch <= pos - in + slack) {
         a.wide.joins[4 * b] = n;
         a.wide.joins[4 * b + 1] = hk;
         a.wide.joins[4 * b + 3] = r0;
-        a.wide.joins[4 * b + 2] = 1 + int32_t((tiles - t0 + stretch - 1) / stretch);
+        a.wide.joins[4 * b + 2] = 2 + int32_t((size - in - slack - 1) / stretch);
       }
     }
-    pos += t1 - t0;
+    pos += out - in;
     rest = 0;
     if (++rt >= count) {
       rt = 0;
@@ -1101,8 +1158,9 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
     sched_kernel<W::kRows, W::kKeys><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
-  const unsigned rows = p.wide ? W::kRows * D / 1024 : unsigned(most_rows(s));
-  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), rows), 256, 0, st>>>(a);
+  // One pass over the rows: reading a piece takes 2 to 3 us, most of it latency.
+  const int64_t rows = p.wide ? W::kRows * D / 1024 : most_rows(s);
+  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), unsigned(rows)), 256, 0, st>>>(a);
 }
 
 // Calls f<E, D>(...) for the shape's type and head width.

@@ -21,7 +21,7 @@ inline bool valid_pages(const rglru_paged_shape_t& s) {
 
 inline bool valid_table(const rglru_paged_shape_t& s) {
   return s.n_seqs >= 1 && s.n_seqs <= kMaxSeqs && s.max_pages >= 1 &&
-         s.max_pages < (int64_t(1) << 31) / s.page_size && s.max_new >= 0;
+         s.max_pages <= ((int64_t(1) << 31) - (1 << 16)) / s.page_size && s.max_new >= 0;  // tiles may reach past the end
 }
 
 inline bool valid_io(const rglru_paged_shape_t& s) {
