@@ -254,6 +254,10 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// Keeps the compiler from moving anything across: left to itself it saves registers by putting every LDS read right
+// before its product and waits for each.
+__device__ __forceinline__ void order() { __builtin_amdgcn_sched_barrier(0); }
+
 // Waits until this wave's LDS reads have returned, before their place is loaded anew.
 __device__ __forceinline__ void wait_reads() {
   __builtin_amdgcn_s_waitcnt(0xC07F);
@@ -315,31 +319,35 @@ struct Wave {
     const int h = lane >> 5;
     f32x16 s[BN / 32];
     {
+      // product i: keys of subtile i / (D / 16), elements 16 (i % (D / 16)) on; operands are read kAhead products early
+      constexpr int kSteps = D / 16, kAll = BN / 32 * kSteps, kAhead = 4;
       const int r = lane & 31;
       const int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
-#pragma unroll
-      for (int b = 0; b < BN / 32; ++b) {
-        s[b] = 0.0f;
-#pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          Frag<E> k;
-          const lds_u8* p = kt + b * 32 * L::kRowBytes;
-          if constexpr (sizeof(E) == 2) {
-            k.w = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 32)));
-          } else {
-            const u32x4 w0 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64)));
-            const u32x4 w1 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64 + 16)));
-            k.w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
-          }
-          if constexpr (kQLds == 0) {
-            s[b] = mma(k, q[x], s[b]);
-          } else {
-            Frag<E> f;
-            if (x < kQRegs) f = q[x < kQRegs ? x : 0];
-            else f.w = *(const __attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16);
-            s[b] = mma(k, f, s[b]);
-          }
+      Frag<E> k[kAhead], f[kQLds > 0 ? kAhead : 1];
+      auto fetch = [&](int i) {
+        const int b = i / kSteps, x = i % kSteps;
+        const lds_u8* p = kt + b * 32 * L::kRowBytes;
+        if constexpr (sizeof(E) == 2) {
+          k[i % kAhead].w = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 32)));
+        } else {
+          const u32x4 w0 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64)));
+          const u32x4 w1 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64 + 16)));
+          k[i % kAhead].w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
+        if constexpr (kQLds > 0)
+          if (x >= kQRegs) f[i % kAhead].w = *(const __attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16);
+      };
+#pragma unroll
+      for (int b = 0; b < BN / 32; ++b) s[b] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(i);
+#pragma unroll
+      for (int i = 0; i < kAll; ++i) {
+        const int b = i / kSteps, x = i % kSteps;
+        if (kQLds > 0 && x >= kQRegs) s[b] = mma(k[i % kAhead], f[kQLds > 0 ? i % kAhead : 0], s[b]);
+        else s[b] = mma(k[i % kAhead], q[x < kQRegs ? x : 0], s[b]);
+        if (i + kAhead < kAll) fetch(i + kAhead);
+        order();
       }
     }
     done();
@@ -390,10 +398,16 @@ struct Wave {
   // Adds BN weighted values to the output.
   template <int BN>
   __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane) {
+    constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = 4;
+    Frag<E> v[kAhead];
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x)
+    for (int i = 0; i < kAhead; ++i) v[i] = value_frag(vt, i / kSteps, i % kSteps, lane);
 #pragma unroll
-      for (int y = 0; y < BN / 16; ++y) o[x] = mma(value_frag(vt, x, y, lane), p[y], o[x]);
+    for (int i = 0; i < kAll; ++i) {
+      o[i / kSteps] = mma(v[i % kAhead], p[i % kSteps], o[i / kSteps]);
+      if (i + kAhead < kAll) v[i % kAhead] = value_frag(vt, (i + kAhead) / kSteps, (i + kAhead) % kSteps, lane);
+      order();
+    }
   }
 
   __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int lane) const {
