@@ -254,6 +254,9 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("" ::: "memory");
 }
 
+// Hides where a value comes from: what is computed of it is computed here, and not kept in registers across tiles.
+__device__ __forceinline__ void fresh_value(int& x) { asm volatile("" : "+v"(x)); }
+
 // Keeps the compiler from moving anything across: left to itself it saves registers by putting every LDS read right
 // before its product and waits for each.
 __device__ __forceinline__ void order() { __builtin_amdgcn_sched_barrier(0); }
@@ -264,14 +267,11 @@ __device__ __forceinline__ void wait_reads() {
   asm volatile("" ::: "memory");
 }
 
-// 32 rows of one wave. The last kQLds of the D / 16 query operands stay in LDS (`qs`, 1 KB each), the others in registers.
-template <typename E, int D, int kQLds>
+// 32 rows of one wave.
+template <typename E, int D>
 struct Wave {
   using L = Tile<E, D>;
-  static constexpr int kQRegs = D / 16 - kQLds;
-  static_assert(kQLds == 0 || sizeof(E) == 2, "16 bytes per lane");
-  Frag<E> q[kQRegs];
-  lds_u8* qs;
+  Frag<E> q[D / 16];
   f32x16 o[D / 32];
   float m, c, l;     // running maximum of the scores, the same times scale2 (log2 units), sum of the weights (this half-wave's keys)
   int32_t lo, hi;    // the keys this lane's row sees: lo <= j <= hi
@@ -281,19 +281,15 @@ struct Wave {
     const int32_t t = live ? r / a.group : 0, g = live ? r - t * a.group : 0;
     const uint8_t* src = a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + g) * D) * sizeof(E);
     const int h = lane >> 5;
-    const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
-      Frag<E> f;
-      f.w = 0;
-      if (live) f = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
-      f.w = (f.w & keep) ^ flip;
-      if constexpr (kQLds == 0) {
-        q[x] = f;
-      } else {
-        if (x < kQRegs) q[x < kQRegs ? x : 0] = f;
-        else *(__attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16) = f.w;
-      }
+      q[x].w = 0;
+      if (live) q[x] = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
+    }
+    if (a.q_sign <= 0) {
+      const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x) q[x].w = (q[x].w & keep) ^ flip;
     }
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
@@ -322,8 +318,9 @@ struct Wave {
       // product i: keys of subtile i / (D / 16), elements 16 (i % (D / 16)) on; operands are read kAhead products early
       constexpr int kSteps = D / 16, kAll = BN / 32 * kSteps, kAhead = 4;
       const int r = lane & 31;
-      const int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
-      Frag<E> k[kAhead], f[kQLds > 0 ? kAhead : 1];
+      int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
+      fresh_value(at);
+      Frag<E> k[kAhead];
       auto fetch = [&](int i) {
         const int b = i / kSteps, x = i % kSteps;
         const lds_u8* p = kt + b * 32 * L::kRowBytes;
@@ -334,8 +331,6 @@ struct Wave {
           const u32x4 w1 = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 64 + 16)));
           k[i % kAhead].w = __builtin_shufflevector(w0, w1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
-        if constexpr (kQLds > 0)
-          if (x >= kQRegs) f[i % kAhead].w = *(const __attribute__((address_space(3))) u32x4*)(qs + ((x - kQRegs) * 64 + lane) * 16);
       };
 #pragma unroll
       for (int b = 0; b < BN / 32; ++b) s[b] = 0.0f;
@@ -344,8 +339,7 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < kAll; ++i) {
         const int b = i / kSteps, x = i % kSteps;
-        if (kQLds > 0 && x >= kQRegs) s[b] = mma(k[i % kAhead], f[kQLds > 0 ? i % kAhead : 0], s[b]);
-        else s[b] = mma(k[i % kAhead], q[x < kQRegs ? x : 0], s[b]);
+        s[b] = mma(k[i % kAhead], q[x], s[b]);
         if (i + kAhead < kAll) fetch(i + kAhead);
         order();
       }
@@ -399,39 +393,47 @@ struct Wave {
   template <int BN>
   __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane) {
     constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = 4;
+    int start = value_at(lane);
+    fresh_value(start);
     Frag<E> v[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) v[i] = value_frag(vt, i / kSteps, i % kSteps, lane);
+    for (int i = 0; i < kAhead; ++i) v[i] = value_frag(vt, i / kSteps, i % kSteps, start);
 #pragma unroll
     for (int i = 0; i < kAll; ++i) {
       o[i / kSteps] = mma(v[i % kAhead], p[i % kSteps], o[i / kSteps]);
-      if (i + kAhead < kAll) v[i % kAhead] = value_frag(vt, (i + kAhead) / kSteps, (i + kAhead) % kSteps, lane);
+      if (i + kAhead < kAll) v[i % kAhead] = value_frag(vt, (i + kAhead) / kSteps, (i + kAhead) % kSteps, start);
       order();
     }
   }
 
-  __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int lane) const {
-    Frag<E> v;
+  // Where a lane's values start: bf16, row 4h + (lane % 16) / 4, columns 16 ((lane / 16) % 2) + 4 (lane % 4) .., of which the
+  // transposing read hands the lane 4 rows of column lane % 32; float32, row 4h, column lane % 32.
+  __device__ static __forceinline__ int value_at(int lane) {
     const int h = lane >> 5;
     if constexpr (sizeof(E) == 2) {
-      // lane -> row 4h + (lane % 16) / 4, columns 16 ((lane / 16) % 2) + 4 (lane % 4) ..: the transposing read hands
-      // the lane 4 rows of column lane % 32
-      const int r = 4 * h + (lane & 15) / 4;
-      const int col = 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
-      const int at = r * L::kRowBytes + ((4 * x + col) ^ L::swz_v(r)) * 16 + (lane & 1) * 8 + y * 16 * L::kRowBytes;
+      const int r = 4 * h + (lane & 15) / 4, col = 2 * ((lane >> 4) & 1) + (lane & 3) / 2;
+      return r * L::kRowBytes + (col ^ L::swz_v(r)) * 16 + (lane & 1) * 8;
+    } else {
+      const int r = 4 * h, col = lane & 31;
+      return r * L::kRowBytes + ((col / 4) ^ L::swz_v(r)) * 16 + (col % 4) * 4;
+    }
+  }
+
+  // The operand of columns 32 x .. and keys 16 y .. of a tile. 32 columns are 4 (8) pieces of a row, which the swizzle
+  // takes to others of the row's pieces: an XOR.
+  __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int start) const {
+    Frag<E> v;
+    const int at = (start ^ (x * 32 * int(sizeof(E)))) + y * 16 * L::kRowBytes;
+    if constexpr (sizeof(E) == 2) {
       const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + at));
       const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
           (__attribute__((address_space(3))) s16x4*)(vt + at + 8 * L::kRowBytes));
       const u32x2 a = __builtin_bit_cast(u32x2, v0), b = __builtin_bit_cast(u32x2, v1);
       v.w = __builtin_shufflevector(a, b, 0, 1, 2, 3);
     } else {
-      const int col = 32 * x + (lane & 31);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int r = y * 16 + 8 * (j / 4) + 4 * h + j % 4;
-        const int at = r * L::kRowBytes + (((col / 4) ^ L::swz_v(r)) * 16) + (col % 4) * 4;
-        v.w[j] = *(const __attribute__((address_space(3))) uint32_t*)(vt + at);
-      }
+      for (int j = 0; j < 8; ++j)
+        v.w[j] = *(const __attribute__((address_space(3))) uint32_t*)(vt + at + (8 * (j / 4) + j % 4) * L::kRowBytes);
     }
     return v;
   }
@@ -457,7 +459,7 @@ struct Wave {
       for (uint32_t sign = 0; sign < 2; ++sign) {
         f32x16 sum = 0.0f;
 #pragma unroll
-        for (int y = 0; y < BN / 16; ++y) sum = mma(marks(value_frag(vt, x, y, lane), sign), see[y], sum);
+        for (int y = 0; y < BN / 16; ++y) sum = mma(marks(value_frag(vt, x, y, value_at(lane)), sign), see[y], sum);
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[x][r] += sum[r] > 0.0f ? (sign ? -INFINITY : INFINITY) : 0.0f;
       }
@@ -612,7 +614,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   }
   int n = __builtin_amdgcn_readfirstlane(found_seq);
   int64_t rest = found_rest;   // position within the sequence's units
-  Wave<E, D, 0> w;
+  Wave<E, D> w;
   lds_u8* const mine = (lds_u8*)buf + wave * 4 * P::kTileBytes;
   while (pos < end && n < a.N) {
     const Seq s = seq_of(a, n);
@@ -856,25 +858,25 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
 template <typename E, int D>
 struct Wide {
   static constexpr bool kBf16 = sizeof(E) == 2;
-  // two waves per SIMD, so that one's softmax runs beside the other's products, where the registers allow: bf16 with
-  // D = 256 keeps half of its queries in LDS for that
+  // two waves per SIMD, so that one's softmax runs beside the other's products, where the registers allow
   static constexpr int kWaves = kBf16 || D == 64 ? 8 : 4;
   static constexpr int kThreads = kWaves * 64;
   static constexpr int kRows = kWaves * 32;
   static constexpr int kKeys = D == 256 || (D == 128 && !kBf16) ? 32 : 64;
-  static constexpr int kQLds = kBf16 && D == 256 ? 8 : 0;
+  // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
+  // (D = 128); float32 tiles take 16 times as long.
+  static constexpr int kOver = !kBf16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
   static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
   static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
 };
 
-constexpr int kWideOver = 2;
 constexpr int kSlackPart = 16;  // a cut moves by up to a sixteenth of a stretch
 
 // The row tiles of all sequences: sched[0] their number, sched[1] the length
 // of one key head's units, then for each tile the length before it and (sequence << 32 | row tile).
 constexpr int kSchedThreads = 1024;
 
-template <int kRows, int kKeys>
+template <int kRows, int kKeys, int kOver>
 __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
   __shared__ int64_t part[kSchedThreads / 64];
   const int tid = threadIdx.x;
@@ -903,10 +905,13 @@ __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
         if (starts[mid] <= t) lo = mid; else hi = mid - 1;
       }
       const Seq s = seq_of(a, lo);
-      const int32_t r0 = int32_t(t - starts[lo]) * kRows;
+      // first, last, second, last but one ..: under a causal mask the first see few keys and the last many, and in this
+      // order stretches of one length are whole units more often
+      const int32_t i = int32_t(t - starts[lo]), all = (s.fresh * a.group + kRows - 1) / kRows;
+      const int32_t rt = i % 2 == 0 ? i / 2 : all - 1 - i / 2, r0 = rt * kRows;
       const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
-      v = x.hi - x.lo + kWideOver;
-      which[t] = int64_t(lo) << 32 | (t - starts[lo]);
+      v = x.hi - x.lo + kOver;
+      which[t] = int64_t(lo) << 32 | rt;
     }
     const int64_t inc = total + block_scan<kSchedThreads>(v, part, sum);
     if (t < count) before[t] = inc - v;
@@ -922,14 +927,13 @@ template <typename E, int D>
 __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
   using P = Wide<E, D>;
   __shared__ __align__(1024) unsigned char buf[4 * P::kTileBytes];
-  __shared__ __align__(16) unsigned char queries[P::kQLds > 0 ? P::kWaves * P::kQLds * 1024 : 16];
   __shared__ int odd_waves[P::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
   const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
   const int64_t count = a.sched[0], per_head = a.sched[1];
   const int64_t total = per_head * a.Hkv;
-  const int64_t stretch = stretch_of(total, a.wide.grid, 1 + kWideOver);
+  const int64_t stretch = stretch_of(total, a.wide.grid, 1 + P::kOver);
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
   const int64_t* const before = a.sched + 2;
   const int64_t* const which = before + a.max_tiles;
@@ -952,7 +956,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   };
   // A cut costs a write and a read of a whole output tile, so one that falls near an end of a unit moves there (and one
   // in its fixed part always).
-  const int64_t slack = max(stretch / kSlackPart, int64_t(kWideOver));
+  const int64_t slack = max(stretch / kSlackPart, int64_t(P::kOver));
   auto snap = [&](int64_t at, int64_t start, int64_t size) {
     const int64_t off = at - start;
     return off <= size - off ? (off <= slack ? start : at) : (size - off <= slack ? start + size : at);
@@ -972,9 +976,8 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     if (++rt >= count) rt = 0, ++hk;
   }
   int64_t rest = pos - start;
-  Wave<E, D, P::kQLds> w;
+  Wave<E, D> w;
   lds_u8* const tiles_at = (lds_u8*)buf;
-  w.qs = (lds_u8*)queries + (P::kQLds > 0 ? wave * P::kQLds * 1024 : 0);
   while (pos < end) {
     const int64_t id = which[rt];
     const int n = __builtin_amdgcn_readfirstlane(int(id >> 32));
@@ -982,16 +985,15 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     const int32_t rows = s.fresh * a.group;
     const int32_t r0 = __builtin_amdgcn_readfirstlane(int(id & 0xFFFFFFFF)) * P::kRows;
     const Span x = span_of<P::kKeys>(a, s, r0, max(min(r0 + P::kRows, rows) - 1, r0));
-    const int32_t tiles = x.hi - x.lo, size = tiles + kWideOver;
+    const int32_t tiles = x.hi - x.lo, size = tiles + P::kOver;
     const int32_t in = __builtin_amdgcn_readfirstlane(int32_t(rest));   // where this stretch enters the unit and leaves it
     const int32_t out = __builtin_amdgcn_readfirstlane(int32_t(min(int64_t(size), in + (end - pos))));
-    const int32_t t0 = max(in - kWideOver, 0), t1 = max(out - kWideOver, 0);
+    const int32_t t0 = max(in - P::kOver, 0), t1 = max(out - P::kOver, 0);
     const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
     const int32_t w0 = r0 + wave * 32;   // this wave's rows
     const bool busy = w0 < rows;
     const Span mine = span_of<P::kKeys>(a, s, min(w0, rows - 1), min(w0 + 31, rows - 1));
-    w.start(a, s, hk, w0 + (lane & 31), rows, lane);
 
     // this wave's share of a tile: rows mine_at .., all in one page, looked up one tile ahead
     constexpr int kMine = P::kKeys / P::kWaves;
@@ -1007,6 +1009,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     };
     uint32_t half = 0;
     load(t0, uint32_t(uintptr_t(tiles_at)));
+    w.start(a, s, hk, w0 + (lane & 31), rows, lane);
     for (int32_t t = t0; t < t1; ++t) {
       wait_loads<0>();
       __syncthreads();   // the tile is there, and every wave is done with the other buffer
@@ -1169,7 +1172,7 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
   a.least_rows = p.narrow ? kNarrowRows : 0;
   if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid), Narrow<E, D>::kThreads, 0, st>>>(a);
   if (p.wide) {
-    sched_kernel<W::kRows, W::kKeys><<<1, kSchedThreads, 0, st>>>(a);
+    sched_kernel<W::kRows, W::kKeys, W::kOver><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
   // One pass over the rows: reading a piece takes 2 to 3 us, most of it latency.
