@@ -520,9 +520,17 @@ constexpr int part_floats(int rows) {
 // go to `parts` (slot 0: the unit began in an earlier stretch, slot 1: it began
 // here) and the join after the cut merges them in order, so the bits do not
 // depend on timing. A cut within the fixed part moves to the unit's start.
-__device__ __forceinline__ int64_t stretch_of(int64_t total, int grid, int least) {
-  return max((total + grid - 1) / grid, int64_t(least));
-}
+struct Line {
+  int64_t total;
+  int32_t parts;  // stretches
+  __device__ __forceinline__ Line(int64_t total_, int grid, int least) : total(total_) {
+    parts = int(min(max(total / least, int64_t(1)), int64_t(grid)));
+  }
+  // Where stretch b starts.
+  __device__ __forceinline__ int64_t start(int64_t b) const { return total * min(b, int64_t(parts)) / parts; }
+  // Stretches that start before `at`.
+  __device__ __forceinline__ int64_t before(int64_t at) const { return (at * parts + total - 1) / total; }
+};
 
 // ---- few rows: at most 32 per unit (decode steps, drafts) ----
 //
@@ -591,10 +599,11 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     total += sum;
   }
   total *= a.Hkv;
-  const int64_t stretch = stretch_of(total, a.narrow.grid, P::kWaves + kNarrowOver);
-  int64_t pos = b * stretch;
-  const int64_t end = min(pos + stretch, total);
   if (tid == 0) a.narrow.joins[4 * b + 2] = 0;
+  if (total == 0) return;
+  const Line line(total, a.narrow.grid, P::kWaves + kNarrowOver);
+  int64_t pos = line.start(b);
+  const int64_t end = line.start(b + 1);
   if (pos >= end) return;
   {
     int64_t before = 0;
@@ -761,12 +770,12 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       }
       __syncthreads();
     }
-    if (tid == 0 && t0 > 0 && (b - 1) * stretch <= pos - in + kNarrowOver) {
+    if (tid == 0 && t0 > 0 && line.start(b - 1) <= pos - in + kNarrowOver) {
       // the first cut of this unit: the one before is not within it
       a.narrow.joins[4 * b] = n;
       a.narrow.joins[4 * b + 1] = hk;
       a.narrow.joins[4 * b + 3] = 0;
-      a.narrow.joins[4 * b + 2] = 1 + int32_t((size - in + stretch - 1) / stretch);
+      a.narrow.joins[4 * b + 2] = int32_t(1 + line.before(pos - in + size) - b);
     }
     pos += out - in;
     rest = out < size ? rest + (out - in) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * size : 0);
@@ -777,9 +786,11 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
 // Merges the pieces of every unit that was cut, in the order of the keys. A
 // row takes D / 4 threads; the other threads of a workgroup take further rows
 // or, where there are many pieces, further pieces of the same row.
+constexpr int kJoinThreads = 256;
+
 template <typename E, int D, int kWideRows>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  constexpr int kLanes = D / 4, kSets = 256 / kLanes, kAhead = 4, kShare = 16;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
+  constexpr int kLanes = D / 4, kSets = kJoinThreads / kLanes, kAhead = 4, kShare = 16;
   __shared__ float4 acc_s[kSets][kLanes];
   __shared__ float l_s[kSets], c_s[kSets];
   const bool wide = int(blockIdx.x) < a.wide.grid;
@@ -933,8 +944,9 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
   const int64_t count = a.sched[0], per_head = a.sched[1];
   const int64_t total = per_head * a.Hkv;
-  const int64_t stretch = stretch_of(total, a.wide.grid, 1 + P::kOver);
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
+  if (total == 0) return;
+  const Line line(total, a.wide.grid, 1 + P::kOver);
   const int64_t* const before = a.sched + 2;
   const int64_t* const which = before + a.max_tiles;
   // The unit that holds position `at`: key head, row tile, start.
@@ -956,20 +968,20 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   };
   // A cut costs a write and a read of a whole output tile, so one that falls near an end of a unit moves there (and one
   // in its fixed part always).
-  const int64_t slack = max(stretch / kSlackPart, int64_t(P::kOver));
+  const int64_t slack = max(total / line.parts / kSlackPart, int64_t(P::kOver));
   auto snap = [&](int64_t at, int64_t start, int64_t size) {
     const int64_t off = at - start;
     return off <= size - off ? (off <= slack ? start : at) : (size - off <= slack ? start + size : at);
   };
   int hk, rt, other_hk, other_rt;
-  int64_t start, length, pos = total, end = total;
-  if ((b + 1) * stretch < total) {
-    find((b + 1) * stretch, other_hk, other_rt, start, length);
-    end = snap((b + 1) * stretch, start, length);
+  int64_t start, length, pos = line.start(b), end = line.start(b + 1);
+  if (pos >= total) return;
+  if (end < total) {
+    find(end, other_hk, other_rt, start, length);
+    end = snap(end, start, length);
   }
-  if (b * stretch >= total) return;
-  find(b * stretch, hk, rt, start, length);
-  pos = snap(b * stretch, start, length);
+  find(pos, hk, rt, start, length);
+  pos = snap(pos, start, length);
   if (pos >= end) return;
   if (pos == start + length) {
     start = pos;
@@ -1073,11 +1085,11 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
         }
       }
       // the first cut of this unit: the one before is not within it (or has moved to its start)
-      if (tid == 0 && t0 > 0 && (b - 1) * stretch <= pos - in + slack) {
+      if (tid == 0 && t0 > 0 && line.start(b - 1) <= pos - in + slack) {
         a.wide.joins[4 * b] = n;
         a.wide.joins[4 * b + 1] = hk;
         a.wide.joins[4 * b + 3] = r0;
-        a.wide.joins[4 * b + 2] = 2 + int32_t((size - in - slack - 1) / stretch);
+        a.wide.joins[4 * b + 2] = int32_t(1 + line.before(pos - in + size - slack) - b);
       }
     }
     pos += out - in;
@@ -1175,9 +1187,10 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
     sched_kernel<W::kRows, W::kKeys, W::kOver><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
-  // One pass over the rows: reading a piece takes 2 to 3 us, most of it latency.
-  const int64_t rows = p.wide ? W::kRows * D / 1024 : most_rows(s);
-  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), unsigned(rows)), 256, 0, st>>>(a);
+  // One pass over the rows: a pass costs the latency of its reads, 2 to 3 us.
+  constexpr int kPass = kJoinThreads * 4 / D;
+  const unsigned parts = unsigned(p.wide ? ceil_div(W::kRows, kPass) : most_rows(s));
+  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), parts), kJoinThreads, 0, st>>>(a);
 }
 
 // Calls f<E, D>(...) for the shape's type and head width.

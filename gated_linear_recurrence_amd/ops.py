@@ -8,6 +8,7 @@ HIP kernels; nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
 import weakref
 from typing import Optional
 
@@ -27,6 +28,8 @@ def _stream(device: torch.device):
 
 
 def _need(t, name, shape, dtype, device):
+    if type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.shape == shape and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device != device:
@@ -602,6 +605,28 @@ def rglru_delta_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: 
     return o, final_state
 
 
+_paged_shape = functools.lru_cache(maxsize=1024)(_lib.rglru_paged_shape_t)   # by its fields; the library only reads it
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_attn_bytes(*fields) -> int:
+    return int(_lib.load().rglru_paged_attn_workspace_bytes(ctypes.byref(_paged_shape(*fields))))
+
+
+def _call_on(device, fn, where, *args):
+    """Calls a library function on the current stream of `device` (made current for it where another one is)."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _lib.check(status, where)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _paged_cache(k_cache, v_cache, device):
     """Checks a page cache pair; returns its shape [n_pages, Hkv, page_size, D]."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
@@ -680,20 +705,22 @@ def rglru_page_plan(context_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_
     _need(free_pages, "free_pages", (n_pages,), torch.int32, dev)
     _need(free_count, "free_count", (1,), torch.int32, dev)
     t = int(n_tokens)
-    slot_map = _out(slot_map, "slot_map", (t,), torch.int32, dev)
-    positions = _out(positions, "positions", (t,), torch.int32, dev)
-    kv_lens = _out(kv_lens, "kv_lens", (n,), torch.int32, dev)
-    held_lens_out = _out(held_lens_out, "held_lens_out", (n,), torch.int32, dev)
-    free_count_out = _out(free_count_out, "free_count_out", (1,), torch.int32, dev)
-    unserved = _out(unserved, "unserved", (1,), torch.int32, dev)
-    shape = _lib.rglru_paged_shape_t(t, n_pages, n, width, int(page_size), 0, 0, 0, 0, int(max_new), 0, 0.0, 0, 0)
-    with torch.cuda.device(dev):
-        st = lib.rglru_page_plan(ctypes.byref(shape), _ptr(context_lens), _ptr(held_lens), _ptr(cu_seqlens),
-                                 _ptr(block_table), _ptr(free_pages), _ptr(free_count), _ptr(free_count_out),
-                                 _ptr(slot_map), _ptr(positions), _ptr(kv_lens), _ptr(held_lens_out), _ptr(unserved),
-                                 _stream(dev))
-    _lib.check(st, "rglru_page_plan")
-    return slot_map, positions, kv_lens, held_lens_out, free_count_out, unserved
+    shape = _paged_shape(t, n_pages, n, width, int(page_size), 0, 0, 0, 0, int(max_new), 0, 0.0, 0, 0)
+    if t < 0:
+        raise ValueError("n_tokens must not be negative")
+    outs = (slot_map, positions, kv_lens, held_lens_out, free_count_out, unserved)
+    sizes = (t, t, n, n, 1, 1)
+    if outs.count(None) == 6:   # pieces of one allocation
+        outs = torch.empty(2 * t + 2 * n + 2, dtype=torch.int32, device=dev).split_with_sizes(sizes)
+    else:
+        names = ("slot_map", "positions", "kv_lens", "held_lens_out", "free_count_out", "unserved")
+        outs = tuple(_out(o, k, (m,), torch.int32, dev) for o, k, m in zip(outs, names, sizes))
+    slot_map, positions, kv_lens, held_lens_out, free_count_out, unserved = outs
+    _call_on(dev, lib.rglru_page_plan, "rglru_page_plan", ctypes.byref(shape), context_lens.data_ptr(), _addr(held_lens),
+             cu_seqlens.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+             free_count_out.data_ptr(), slot_map.data_ptr(), positions.data_ptr(), kv_lens.data_ptr(),
+             held_lens_out.data_ptr(), unserved.data_ptr())
+    return outs
 
 
 def rglru_paged_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -710,11 +737,9 @@ def rglru_paged_kv_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor
     if tv != t or row_v != row:
         raise ValueError("k and v must have the same rows")
     _need(slot_map, "slot_map", (t,), torch.int32, dev)
-    shape = _lib.rglru_paged_shape_t(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[k_cache.dtype], 0, 0, 0.0, 0, row)
-    with torch.cuda.device(dev):
-        st = lib.rglru_paged_kv_write(ctypes.byref(shape), _ptr(k), _ptr(v), _ptr(k_cache), _ptr(v_cache),
-                                      _ptr(slot_map), _stream(dev))
-    _lib.check(st, "rglru_paged_kv_write")
+    shape = _paged_shape(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[k_cache.dtype], 0, 0, 0.0, 0, row)
+    _call_on(dev, lib.rglru_paged_kv_write, "rglru_paged_kv_write", ctypes.byref(shape), k.data_ptr(), v.data_ptr(),
+             k_cache.data_ptr(), v_cache.data_ptr(), slot_map.data_ptr())
 
 
 def rglru_paged_attn_workspace_bytes(shape: _lib.rglru_paged_shape_t) -> int:
@@ -748,16 +773,12 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if want_lse or lse is not None:
         lse = _out(lse, "lse", (t, hq), torch.float32, dev)
     sc = (1.0 / float(dim) ** 0.5) if scale is None else float(scale)
-    shape = _lib.rglru_paged_shape_t(t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], int(max_new),
-                                     int(window), sc, row, 0)
+    fields = (t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], int(max_new), int(window), sc, row, 0)
     if workspace is None:
-        nbytes = int(lib.rglru_paged_attn_workspace_bytes(ctypes.byref(shape)))
-        workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(_paged_attn_bytes(*fields), 1), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    with torch.cuda.device(dev):
-        st = lib.rglru_paged_attn_fwd(ctypes.byref(shape), _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), _ptr(q),
-                                      _ptr(k_cache), _ptr(v_cache), _ptr(o), _ptr(lse), _ptr(workspace),
-                                      workspace.numel(), _stream(dev))
-    _lib.check(st, "rglru_paged_attn_fwd")
+    _call_on(dev, lib.rglru_paged_attn_fwd, "rglru_paged_attn_fwd", ctypes.byref(_paged_shape(*fields)),
+             cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel())
     return o, lse
