@@ -97,6 +97,10 @@ __device__ __forceinline__ uint32_t odd_bits(uint32_t w, float) {
   return (w & 0x7F800000u) == 0x7F800000u ? ~0u : 0u;
 }
 
+// The same as a test: the top bits of what this returns.
+__device__ __forceinline__ uint32_t odd_carry(uint32_t w, uint16_t) { return (w & 0x7F807F80u) + 0x00800080u; }
+__device__ __forceinline__ uint32_t odd_carry(uint32_t w, float) { return (w & 0x7F800000u) + 0x00800000u; }
+
 // A 0/1 operand that marks +inf and NaN (sign 0) or -inf and NaN (sign 1).
 __device__ __forceinline__ Frag<uint16_t> marks(const Frag<uint16_t>& f, uint32_t sign) {
   Frag<uint16_t> m;
@@ -170,8 +174,8 @@ struct AttnArgs {
   float* lse;
   int64_t* sched;   // the row tiles of the wide kernel (see sched_kernel)
   Cuts narrow, wide;
-  int64_t T, q_stride;
-  int32_t n_pages, N, width, lps, Hq, Hkv, group, window, max_tiles;
+  int64_t q_stride;
+  int32_t T, n_pages, N, width, lps, Hq, Hkv, group, window, max_tiles;
   int32_t least_rows;  // the wide kernel's sequences have more rows than this
   float scale2;     // |scale| log2 e (1 for a scale of 0, whose queries are zeroed)
   int32_t q_sign;   // sign of the scale: -1, 0, 1
@@ -183,11 +187,9 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int n) {
   Seq s;
-  const int64_t c0 = min(max(int64_t(a.cu[n]), int64_t(0)), a.T);
-  const int64_t c1 = min(max(int64_t(a.cu[n + 1]), c0), a.T);
-  s.start = int32_t(c0);
-  s.fresh = int32_t(c1 - c0);
-  s.kv = int32_t(min(max(int64_t(a.kv_lens[n]), int64_t(0)), (int64_t(a.width) << a.lps)));
+  s.start = min(max(a.cu[n], 0), a.T);
+  s.fresh = min(max(a.cu[n + 1], s.start), a.T) - s.start;
+  s.kv = min(max(a.kv_lens[n], 0), a.width << a.lps);
   return s;
 }
 
@@ -474,9 +476,9 @@ __device__ __forceinline__ bool any_odd(const lds_u8* vt, int thread) {
   for (int i = 0; i < kTileBytes; i += kThreads * 16) {
     const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i + thread * 16);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) odd |= odd_bits(w[j], E{});
+    for (int j = 0; j < 4; ++j) odd |= odd_carry(w[j], E{});
   }
-  return odd != 0;
+  return (odd & Frag<E>::kSigns) != 0;
 }
 
 // Replaces them by 0.
@@ -570,9 +572,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t&
   return v;
 }
 
-// Length of a unit of sequence n in the line.
-__device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, int n) {
-  const Seq s = seq_of(a, n);
+// Length of a unit of a sequence in the line.
+__device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) {
   if (s.fresh == 0 || int64_t(s.fresh) * a.group > kNarrowRows) return 0;
   const Span x = span_of<kNarrowKeys>(a, s, 0, s.fresh * a.group - 1);
   return x.hi - x.lo + kNarrowOver;
@@ -584,52 +585,58 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   constexpr int kLoads = P::kTileBytes / 1024;
   __shared__ __align__(1024) unsigned char buf[2 * P::kWaves * 2 * P::kTileBytes];
   __shared__ int64_t scan_part[P::kWaves];
+  __shared__ Seq found;
   __shared__ int32_t found_seq;
   __shared__ int64_t found_rest;
   __shared__ float merge_c[P::kWaves][32], merge_l[P::kWaves][32];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.x;
 
-  // Total length, then the sequence that holds this stretch's start.
-  int64_t total = 0;
+  // Total length, then the sequence that holds this stretch's start. Up to a sequence per thread both come of one scan.
+  Seq own = {0, 0, 0};
+  int64_t total = 0, size = 0, upto = 0;
   for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
-    const int n = n0 + tid;
     int64_t sum;
-    block_scan<P::kThreads>(n < a.N ? narrow_size(a, n) : 0, scan_part, sum);
+    own = {0, 0, 0};
+    if (n0 + tid < a.N) own = seq_of(a, n0 + tid);
+    size = int64_t(narrow_size(a, own)) * a.Hkv;
+    upto = block_scan<P::kThreads>(size, scan_part, sum);
     total += sum;
   }
-  total *= a.Hkv;
   if (tid == 0) a.narrow.joins[4 * b + 2] = 0;
   if (total == 0) return;
-  const Line line(total, a.narrow.grid, P::kWaves + kNarrowOver);
+  const Line line(total, a.narrow.grid, P::kWaves);
   int64_t pos = line.start(b);
   const int64_t end = line.start(b + 1);
   if (pos >= end) return;
-  {
-    int64_t before = 0;
-    for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
-      const int n = n0 + tid;
-      const int64_t t = n < a.N ? int64_t(narrow_size(a, n)) * a.Hkv : 0;
-      int64_t sum;
-      const int64_t inc = before + block_scan<P::kThreads>(t, scan_part, sum);
-      if (pos >= inc - t && pos < inc) {
-        found_seq = n;
-        found_rest = pos - (inc - t);
-      }
-      before += sum;
-      if (pos < before) break;
+  int64_t found_before = 0;
+  for (int n0 = 0;; n0 += P::kThreads) {
+    int64_t sum = total;
+    if (a.N > P::kThreads) {
+      own = {0, 0, 0};
+      if (n0 + tid < a.N) own = seq_of(a, n0 + tid);
+      size = int64_t(narrow_size(a, own)) * a.Hkv;
+      upto = found_before + block_scan<P::kThreads>(size, scan_part, sum);
     }
-    __syncthreads();
+    if (pos >= upto - size && pos < upto) {
+      found = own;
+      found_seq = n0 + tid;
+      found_rest = pos - (upto - size);
+    }
+    found_before += sum;
+    if (pos < found_before || n0 + P::kThreads >= a.N) break;
   }
+  __syncthreads();
   int n = __builtin_amdgcn_readfirstlane(found_seq);
   int64_t rest = found_rest;   // position within the sequence's units
+  Seq s = {__builtin_amdgcn_readfirstlane(found.start), __builtin_amdgcn_readfirstlane(found.fresh),
+           __builtin_amdgcn_readfirstlane(found.kv)};
   Wave<E, D> w;
   lds_u8* const mine = (lds_u8*)buf + wave * 4 * P::kTileBytes;
   while (pos < end && n < a.N) {
-    const Seq s = seq_of(a, n);
     const int32_t rows = int64_t(s.fresh) * a.group > kNarrowRows ? 0 : s.fresh * a.group;
     if (rows == 0) {
-      ++n;
+      if (++n < a.N) s = seq_of(a, n);
       continue;
     }
     const Span x = span_of<kNarrowKeys>(a, s, 0, rows - 1);
@@ -779,7 +786,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     }
     pos += out - in;
     rest = out < size ? rest + (out - in) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * size : 0);
-    if (out == size && hk + 1 == a.Hkv) ++n;
+    if (out == size && hk + 1 == a.Hkv && ++n < a.N) s = seq_of(a, n);
   }
 }
 
@@ -869,11 +876,12 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
 template <typename E, int D>
 struct Wide {
   static constexpr bool kBf16 = sizeof(E) == 2;
-  // two waves per SIMD, so that one's softmax runs beside the other's products, where the registers allow
-  static constexpr int kWaves = kBf16 || D == 64 ? 8 : 4;
+  // bf16: two waves per SIMD, so that one's softmax runs beside the other's products. float32 products take 16 times as
+  // long and hide the softmax by themselves: one wave per SIMD, half as many rows left idle
+  static constexpr int kWaves = kBf16 ? 8 : 4;
   static constexpr int kThreads = kWaves * 64;
   static constexpr int kRows = kWaves * 32;
-  static constexpr int kKeys = D == 256 || (D == 128 && !kBf16) ? 32 : 64;
+  static constexpr int kKeys = D == 256 || !kBf16 ? 32 : 64;
   // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
   // (D = 128); float32 tiles take 16 times as long.
   static constexpr int kOver = !kBf16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
@@ -946,7 +954,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   const int64_t total = per_head * a.Hkv;
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
   if (total == 0) return;
-  const Line line(total, a.wide.grid, 1 + P::kOver);
+  const Line line(total, a.wide.grid, 1 + P::kOver / 2);
   const int64_t* const before = a.sched + 2;
   const int64_t* const which = before + a.max_tiles;
   // The unit that holds position `at`: key head, row tile, start.
@@ -1241,7 +1249,7 @@ extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, co
   a.vc = static_cast<const uint8_t*>(v_cache);
   a.o = static_cast<uint8_t*>(o);
   a.lse = lse;
-  a.T = s.n_tokens;
+  a.T = int32_t(s.n_tokens);
   a.q_stride = stride;
   a.n_pages = int32_t(s.n_pages);
   a.N = s.n_seqs;
