@@ -579,6 +579,86 @@ __device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) 
   return x.hi - x.lo + kNarrowOver;
 }
 
+// ---- many rows: chunks of a prompt, and whatever stands beside them in a batch ----
+//
+// Bound by the matrix cores. kRows rows of one (sequence, key head) share
+// every tile of kKeys keys and values, which the waves fetch together into one of two LDS
+// buffers while they work on the other; one barrier a tile.
+template <typename E, int D>
+struct Wide {
+  static constexpr bool kBf16 = sizeof(E) == 2;
+  // bf16: two waves per SIMD, so that one's softmax runs beside the other's products. float32 products take 16 times as
+  // long and hide the softmax by themselves: one wave per SIMD, half as many rows left idle
+  static constexpr int kWaves = kBf16 ? 8 : 4;
+  static constexpr int kThreads = kWaves * 64;
+  static constexpr int kRows = kWaves * 32;
+  static constexpr int kKeys = D == 256 || !kBf16 ? 32 : 64;
+  // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
+  // (D = 128); float32 tiles take 16 times as long.
+  static constexpr int kOver = !kBf16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
+  static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
+  static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
+};
+
+// The row tiles of all sequences: sched[0] their number, sched[1] the length
+// of one key head's units, then for each tile the length before it and (sequence << 32 | row tile).
+// One workgroup writes them: the narrow kernel's last, beside the others' work, or a launch of its own where that kernel does not run.
+template <typename W, int kThreads>
+__device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part) {
+  constexpr int kRows = W::kRows, kKeys = W::kKeys, kOver = W::kOver;
+  const int tid = threadIdx.x;
+  int64_t* const before = a.sched + 2;
+  int64_t* const which = before + a.max_tiles;
+  int64_t* const starts = which + a.max_tiles;   // row tiles before each sequence
+  int64_t count = 0, sum;
+  for (int n0 = 0; n0 < a.N; n0 += kThreads) {
+    const int n = n0 + tid;
+    const int64_t rows = n < a.N ? int64_t(seq_of(a, n).fresh) * a.group : 0;
+    const int64_t v = rows > a.least_rows ? (rows + kRows - 1) / kRows : 0;
+    const int64_t inc = count + block_scan<kThreads>(v, part, sum);
+    if (n < a.N) starts[n] = inc - v;
+    count += sum;
+  }
+  count = min(count, int64_t(a.max_tiles));
+  __syncthreads();
+  int64_t total = 0;
+  for (int64_t t0 = 0; t0 < count; t0 += kThreads) {
+    const int64_t t = t0 + tid;
+    int64_t v = 0;
+    if (t < count) {
+      int lo = 0, hi = a.N - 1;  // the last sequence that starts at or before t; empty ones share their start with the next
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+      }
+      const Seq s = seq_of(a, lo);
+      // first, last, second, last but one ..: under a causal mask the first see few keys and the last many, and in this
+      // order stretches of one length are whole units more often
+      const int32_t i = int32_t(t - starts[lo]), all = (s.fresh * a.group + kRows - 1) / kRows;
+      const int32_t rt = i % 2 == 0 ? i / 2 : all - 1 - i / 2, r0 = rt * kRows;
+      const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
+      v = x.hi - x.lo + kOver;
+      which[t] = int64_t(lo) << 32 | rt;
+    }
+    const int64_t inc = total + block_scan<kThreads>(v, part, sum);
+    if (t < count) before[t] = inc - v;
+    total += sum;
+  }
+  if (tid == 0) {
+    a.sched[0] = count;
+    a.sched[1] = total;
+  }
+}
+
+constexpr int kSchedThreads = 1024;
+
+template <typename W>
+__global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
+  __shared__ int64_t part[kSchedThreads / 64];
+  list_row_tiles<W, kSchedThreads>(a, part);
+}
+
+// ---- few rows: the kernel ----
 template <typename E, int D>
 __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnArgs a) {
   using P = Narrow<E, D>;
@@ -591,6 +671,10 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   __shared__ float merge_c[P::kWaves][32], merge_l[P::kWaves][32];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.x;
+  if (b == a.narrow.grid) {
+    list_row_tiles<Wide<E, D>, P::kThreads>(a, scan_part);
+    return;
+  }
 
   // Total length, then the sequence that holds this stretch's start. Up to a sequence per thread both come of one scan.
   Seq own = {0, 0, 0};
@@ -796,13 +880,16 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
 constexpr int kJoinThreads = 256;
 
 template <typename E, int D, int kWideRows>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
-  constexpr int kLanes = D / 4, kSets = kJoinThreads / kLanes, kAhead = 4, kShare = 16;
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide_share, int narrow_share) {
+  constexpr int kLanes = D / 4, kSets = kJoinThreads / kLanes, kAhead = 8, kShare = 16;
   __shared__ float4 acc_s[kSets][kLanes];
   __shared__ float l_s[kSets], c_s[kSets];
-  const bool wide = int(blockIdx.x) < a.wide.grid;
+  // workgroups: `wide_share` for each cut of the wide kernel, then `narrow_share` for each of the narrow one
+  const int wide_blocks = a.wide.grid * wide_share;
+  const bool wide = int(blockIdx.x) < wide_blocks;
   const Cuts& cuts = wide ? a.wide : a.narrow;
-  const int b = wide ? blockIdx.x : blockIdx.x - a.wide.grid, tid = threadIdx.x;
+  const int at = wide ? blockIdx.x : blockIdx.x - wide_blocks, shares = wide ? wide_share : narrow_share;
+  const int b = at / shares, y = at - b * shares, tid = threadIdx.x;
   const int pieces = cuts.joins[4 * b + 2];
   if (pieces == 0) return;
   const int n = cuts.joins[4 * b], hk = cuts.joins[4 * b + 1], r0 = cuts.joins[4 * b + 3];
@@ -835,7 +922,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
     c = top;
   };
   const int step = share ? kSets : 1, side = share ? 1 : kSets;
-  for (int q0 = blockIdx.y * side; q0 < rows; q0 += gridDim.y * side) {
+  for (int q0 = y * side; q0 < rows; q0 += shares * side) {
     const int q = min(q0 + (share ? 0 : set), rows - 1);
     float4 acc = {0, 0, 0, 0};
     float l = 0.0f, c = -INFINITY;
@@ -868,79 +955,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a) {
   }
 }
 
-// ---- many rows: chunks of a prompt, and whatever stands beside them in a batch ----
-//
-// Bound by the matrix cores. kRows rows of one (sequence, key head) share
-// every tile of kKeys keys and values, which the waves fetch together into one of two LDS
-// buffers while they work on the other; one barrier a tile.
-template <typename E, int D>
-struct Wide {
-  static constexpr bool kBf16 = sizeof(E) == 2;
-  // bf16: two waves per SIMD, so that one's softmax runs beside the other's products. float32 products take 16 times as
-  // long and hide the softmax by themselves: one wave per SIMD, half as many rows left idle
-  static constexpr int kWaves = kBf16 ? 8 : 4;
-  static constexpr int kThreads = kWaves * 64;
-  static constexpr int kRows = kWaves * 32;
-  static constexpr int kKeys = D == 256 || !kBf16 ? 32 : 64;
-  // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
-  // (D = 128); float32 tiles take 16 times as long.
-  static constexpr int kOver = !kBf16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
-  static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
-  static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
-};
-
 constexpr int kSlackPart = 16;  // a cut moves by up to a sixteenth of a stretch
-
-// The row tiles of all sequences: sched[0] their number, sched[1] the length
-// of one key head's units, then for each tile the length before it and (sequence << 32 | row tile).
-constexpr int kSchedThreads = 1024;
-
-template <int kRows, int kKeys, int kOver>
-__global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
-  __shared__ int64_t part[kSchedThreads / 64];
-  const int tid = threadIdx.x;
-  int64_t* const before = a.sched + 2;
-  int64_t* const which = before + a.max_tiles;
-  int64_t* const starts = which + a.max_tiles;   // row tiles before each sequence
-  int64_t count = 0, sum;
-  for (int n0 = 0; n0 < a.N; n0 += kSchedThreads) {
-    const int n = n0 + tid;
-    const int64_t rows = n < a.N ? int64_t(seq_of(a, n).fresh) * a.group : 0;
-    const int64_t v = rows > a.least_rows ? (rows + kRows - 1) / kRows : 0;
-    const int64_t inc = count + block_scan<kSchedThreads>(v, part, sum);
-    if (n < a.N) starts[n] = inc - v;
-    count += sum;
-  }
-  count = min(count, int64_t(a.max_tiles));
-  __syncthreads();
-  int64_t total = 0;
-  for (int64_t t0 = 0; t0 < count; t0 += kSchedThreads) {
-    const int64_t t = t0 + tid;
-    int64_t v = 0;
-    if (t < count) {
-      int lo = 0, hi = a.N - 1;  // the last sequence that starts at or before t; empty ones share their start with the next
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (starts[mid] <= t) lo = mid; else hi = mid - 1;
-      }
-      const Seq s = seq_of(a, lo);
-      // first, last, second, last but one ..: under a causal mask the first see few keys and the last many, and in this
-      // order stretches of one length are whole units more often
-      const int32_t i = int32_t(t - starts[lo]), all = (s.fresh * a.group + kRows - 1) / kRows;
-      const int32_t rt = i % 2 == 0 ? i / 2 : all - 1 - i / 2, r0 = rt * kRows;
-      const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
-      v = x.hi - x.lo + kOver;
-      which[t] = int64_t(lo) << 32 | rt;
-    }
-    const int64_t inc = total + block_scan<kSchedThreads>(v, part, sum);
-    if (t < count) before[t] = inc - v;
-    total += sum;
-  }
-  if (tid == 0) {
-    a.sched[0] = count;
-    a.sched[1] = total;
-  }
-}
 
 template <typename E, int D>
 __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
@@ -1190,15 +1205,16 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
   a.sched = reinterpret_cast<int64_t*>(workspace + p.sched);
   a.max_tiles = int32_t(p.max_tiles);
   a.least_rows = p.narrow ? kNarrowRows : 0;
-  if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid), Narrow<E, D>::kThreads, 0, st>>>(a);
+  if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid + p.wide), Narrow<E, D>::kThreads, 0, st>>>(a);
   if (p.wide) {
-    sched_kernel<W::kRows, W::kKeys, W::kOver><<<1, kSchedThreads, 0, st>>>(a);
+    if (!p.narrow) sched_kernel<W><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
-  // One pass over the rows: a pass costs the latency of its reads, 2 to 3 us.
+  // A pass over kPass rows costs the latency of its reads, 2 to 3 us: one pass (rows of few pieces; with many, a row a pass).
   constexpr int kPass = kJoinThreads * 4 / D;
-  const unsigned parts = unsigned(p.wide ? ceil_div(W::kRows, kPass) : most_rows(s));
-  join_kernel<E, D, W::kRows><<<dim3(unsigned(p.narrow_grid + p.wide_grid), parts), kJoinThreads, 0, st>>>(a);
+  const int wide_share = W::kRows / kPass, narrow_share = int(p.wide ? ceil_div(kNarrowRows, kPass) : most_rows(s));
+  join_kernel<E, D, W::kRows><<<unsigned(p.wide_grid * wide_share + p.narrow_grid * narrow_share), kJoinThreads, 0, st>>>(
+      a, wide_share, narrow_share);
 }
 
 // Calls f<E, D>(...) for the shape's type and head width.
