@@ -318,7 +318,7 @@ struct Wave {
     f32x16 s[BN / 32];
     {
       // product i: keys of subtile i / (D / 16), elements 16 (i % (D / 16)) on; operands are read kAhead products early
-      constexpr int kSteps = D / 16, kAll = BN / 32 * kSteps, kAhead = 4;
+      constexpr int kSteps = D / 16, kAll = BN / 32 * kSteps, kAhead = sizeof(E) == 2 ? 4 : 2;
       const int r = lane & 31;
       int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
       fresh_value(at);
@@ -394,7 +394,7 @@ struct Wave {
   // Adds BN weighted values to the output.
   template <int BN>
   __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane) {
-    constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = 4;
+    constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = sizeof(E) == 2 ? 4 : 2;
     int start = value_at(lane);
     fresh_value(start);
     Frag<E> v[kAhead];
@@ -541,16 +541,17 @@ struct Line {
 // the card has some 250. Each wave streams tiles of 32 keys of its own
 // through its own LDS buffers without a barrier; the waves of a workgroup merge
 // at the end of a unit. What counts is how many bytes are in flight: a
-// wave has two buffers of keys and two of values, and asks for the keys (values)
-// after next as soon as it has read those of the present tile.
+// wave asks for the next keys (values) as soon as it has read the buffer that they go to.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
 
 template <typename E, int D>
 struct Narrow {
   static constexpr int kTileBytes = kNarrowKeys * D * int(sizeof(E));
-  // 128 KB of LDS per CU: two workgroups of four waves (D = 64, bf16), or one of as many waves as fit, four at most
-  static constexpr int kWaves = kTileBytes <= 8192 ? 4 : 131072 / (4 * kTileBytes);
-  static constexpr int kGroups = 131072 / (kWaves * 4 * kTileBytes);
+  // 128 KB of LDS per CU, four waves in a workgroup. Up to 8 KB a tile each wave has two buffers of keys and two of
+  // values (and there are two workgroups at 4 KB), at 16 KB one of each, at 32 KB one for both in turn.
+  static constexpr int kWaves = 4;
+  static constexpr int kBuffers = kTileBytes <= 8192 ? 4 : 32768 / kTileBytes;
+  static constexpr int kGroups = kTileBytes == 4096 ? 2 : 1;
   static constexpr int kThreads = kWaves * 64;
 };
 
@@ -663,7 +664,7 @@ template <typename E, int D>
 __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnArgs a) {
   using P = Narrow<E, D>;
   constexpr int kLoads = P::kTileBytes / 1024;
-  __shared__ __align__(1024) unsigned char buf[2 * P::kWaves * 2 * P::kTileBytes];
+  __shared__ __align__(1024) unsigned char buf[P::kWaves * P::kBuffers * P::kTileBytes];
   __shared__ int64_t scan_part[P::kWaves];
   __shared__ Seq found;
   __shared__ int32_t found_seq;
@@ -716,7 +717,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   Seq s = {__builtin_amdgcn_readfirstlane(found.start), __builtin_amdgcn_readfirstlane(found.fresh),
            __builtin_amdgcn_readfirstlane(found.kv)};
   Wave<E, D> w;
-  lds_u8* const mine = (lds_u8*)buf + wave * 4 * P::kTileBytes;
+  lds_u8* const mine = (lds_u8*)buf + wave * P::kBuffers * P::kTileBytes;
   while (pos < end && n < a.N) {
     const int32_t rows = int64_t(s.fresh) * a.group > kNarrowRows ? 0 : s.fresh * a.group;
     if (rows == 0) {
@@ -756,47 +757,52 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
       for (int i = 0; i < kSegs; ++i)
         load_rows<E, D, true, kSegLoads>(a.vc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
     };
-    // mine: keys 0, keys 1, values 0, values 1
-    const uint32_t keys_at = uint32_t(uintptr_t(mine)), values_at = keys_at + 2 * P::kTileBytes;
-    constexpr int kW = P::kWaves;
+    // mine: the buffers of keys, then those of values
+    constexpr int kW = P::kWaves, kTwo = P::kBuffers == 4, kShared = P::kBuffers == 1;
+    constexpr int kValues = kShared ? 0 : P::kBuffers / 2 * P::kTileBytes;
+    const uint32_t keys_at = uint32_t(uintptr_t(mine)), values_at = keys_at + kValues;
     uint32_t half = 0;
     look_up(t0 + wave);
     wait_loads<0>();   // no store of the unit before is counted below
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 1 + kTwo; ++i)
       if (t0 + wave + i * kW < t1) {
         load_keys(t0 + wave + i * kW, keys_at + i * P::kTileBytes);
-        load_values(values_at + i * P::kTileBytes);
+        if (!kShared) load_values(values_at + i * P::kTileBytes);
         look_up(t0 + wave + (i + 1) * kW);
       }
     for (int32_t t = t0 + wave; t < t1; t += kW) {
-      const bool one = t + kW < t1, two = t + 2 * kW < t1;   // further tiles
+      const bool next = t + kW < t1;                // a further tile
+      const bool after = t + (1 + kTwo) * kW < t1;  // and one for the buffers that this tile leaves
       const int32_t kv0 = (x.lo + t) * kNarrowKeys;
       const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
       Frag<E> p[kNarrowKeys / 16];
-      if (one) wait_loads<3 * kLoads>();  // behind these keys: these values, the next tile
-      else wait_loads<kLoads>();
+      // behind these keys are in flight: these values and, of two buffers, the next tile
+      if (kTwo && next) wait_loads<3 * kLoads>();
+      else wait_loads<kShared ? 0 : kLoads>();
       w.template scores<kNarrowKeys>(a, mine + half, kv0, full, lane, p, [&] {
-        if (two) {
-          wait_reads();
-          load_keys(t + 2 * kW, keys_at + half);
-        }
+        if (kShared || after) wait_reads();
+        if (kShared) load_values(values_at);
+        else if (after) load_keys(t + (1 + kTwo) * kW, keys_at + half);
       });
-      if (two) wait_loads<3 * kLoads>();  // behind these values: the next tile, the keys after
-      else if (one) wait_loads<2 * kLoads>();
+      // behind these values: the keys just asked for and, of two buffers, the next tile
+      if (kTwo && after) wait_loads<3 * kLoads>();
+      else if (kTwo && next) wait_loads<2 * kLoads>();
+      else if (!kTwo && !kShared && after) wait_loads<kLoads>();
       else wait_loads<0>();
-      lds_u8* const vt = mine + 2 * P::kTileBytes + half;
+      lds_u8* const vt = mine + kValues + half;
       if (!full && __any(any_odd<E, P::kTileBytes, 64>(vt, lane))) {
         w.template mark<kNarrowKeys>(vt, kv0, lane);
         clean<E, P::kTileBytes, 64>(vt, lane);
       }
       w.template values<kNarrowKeys>(vt, p, lane);
-      if (two) {
+      if (after) {
         wait_reads();
-        load_values(values_at + half);
-        look_up(t + 3 * kW);
+        if (kShared) load_keys(t + kW, keys_at);
+        else load_values(values_at + half);
+        look_up(t + (2 + kTwo) * kW);
       }
-      half ^= P::kTileBytes;
+      if (kTwo) half ^= P::kTileBytes;
     }
 
     // The waves merge: maxima and sums first, then every thread sums some columns over the waves.
