@@ -31,7 +31,7 @@ extern "C" {
  * point checks the fields it reads): 0 <= n_tokens < 2^31; 1 <= n_seqs <=
  * 2^16; page_size a power of two from 8 to 1024; n_pages >= 1 with n_pages *
  * page_size < 2^31; max_pages >= 1 with max_pages * page_size <= 2^31 - 2^16; 1 <= kv_heads <= q_heads <= 2^14 with
- * q_heads a multiple of kv_heads; n_tokens * q_heads < 2^31; head_dim >= 1;
+ * q_heads a multiple of kv_heads; n_tokens * q_heads <= 2^31 - 2^16; head_dim >= 1;
  * io_dtype an rglru_io_t; max_new, window >= 0; a finite scale; strides 0 or
  * at least the dense row. Within them, a head_dim other than 64, 128 or 256
  * is RGLRU_ERR_UNSUPPORTED, and a stride that is not a multiple of 16 bytes
