@@ -163,6 +163,8 @@ struct Cuts {
   int32_t grid;
 };
 
+struct RowTile;
+
 struct AttnArgs {
   const int32_t* cu;
   const int32_t* kv_lens;
@@ -172,7 +174,8 @@ struct AttnArgs {
   const uint8_t* vc;
   uint8_t* o;
   float* lse;
-  int64_t* sched;   // the row tiles of the wide kernel (see sched_kernel)
+  int64_t* sched;   // the row tiles of the wide kernel (see list_row_tiles)
+  RowTile* row_tiles;
   Cuts narrow, wide;
   int64_t q_stride;
   int32_t T, n_pages, N, width, lps, Hq, Hkv, group, window, max_tiles;
@@ -278,7 +281,8 @@ struct Wave {
   float m, c, l;     // running maximum of the scores, the same times scale2 (log2 units), sum of the weights (this half-wave's keys)
   int32_t lo, hi;    // the keys this lane's row sees: lo <= j <= hi
 
-  __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, int hk, int32_t r, int32_t rows, int lane) {
+  // Loads this lane's share of the queries of row r.
+  __device__ __forceinline__ void queries(const AttnArgs& a, const Seq& s, int hk, int32_t r, int32_t rows, int lane) {
     const bool live = r < rows;
     const int32_t t = live ? r / a.group : 0, g = live ? r - t * a.group : 0;
     const uint8_t* src = a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + g) * D) * sizeof(E);
@@ -288,6 +292,9 @@ struct Wave {
       q[x].w = 0;
       if (live) q[x] = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
     }
+  }
+
+  __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, int32_t r, int32_t rows) {
     if (a.q_sign <= 0) {
       const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? Frag<E>::kSigns : 0u;
 #pragma unroll
@@ -297,7 +304,7 @@ struct Wave {
     for (int x = 0; x < D / 32; ++x) o[x] = 0.0f;
     m = c = -INFINITY;
     l = 0.0f;
-    hi = live ? max(s.kv - s.fresh + t, -1) : -1;
+    hi = r < rows ? max(s.kv - s.fresh + r / a.group, -1) : -1;
     lo = a.window > 0 ? max(hi - a.window + 1, 0) : 0;
   }
 
@@ -503,6 +510,29 @@ __device__ __forceinline__ void store4(uint8_t* p, float a, float b, float c, fl
   }
 }
 
+// The D outputs of one row times `f`, 16 bytes per lane and instruction. The two half-waves hold 4 elements each of every
+// 8: for bf16 they trade, so that one has the 8 of an even group and the other those of the next.
+template <typename E, int D>
+__device__ __forceinline__ void store_row(uint8_t* to, const f32x16* o, float f, int h) {
+#pragma unroll
+  for (int y = 0; y < D / 32; ++y)
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = o[y][4 * k + j] * f;
+      if constexpr (sizeof(E) == 2) {
+        const auto a = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(e[0], e[1]), f32x2_to_bf16x2(e[4], e[5]), false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(e[2], e[3]), f32x2_to_bf16x2(e[6], e[7]), false, false);
+        const u32x4 w = {a[0], b[0], a[1], b[1]};
+        *reinterpret_cast<u32x4*>(to + (y * 32 + 8 * (k + h)) * 2) = w;
+      } else {
+        store4<float>(to + (y * 32 + 8 * k + 4 * h) * 4, e[0], e[1], e[2], e[3]);
+        store4<float>(to + (y * 32 + 8 * k + 8 + 4 * h) * 4, e[4], e[5], e[6], e[7]);
+      }
+    }
+}
+
 // Output row of (sequence, key head, row), as an index of [T, Hq].
 __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Seq& s, int hk, int32_t r) {
   const int32_t t = r / a.group;
@@ -602,15 +632,23 @@ struct Wide {
 };
 
 // The row tiles of all sequences: sched[0] their number, sched[1] the length
-// of one key head's units, then for each tile the length before it and (sequence << 32 | row tile).
+// of one key head's units, then for each tile the length before it, then for each its RowTile.
 // One workgroup writes them: the narrow kernel's last, beside the others' work, or a launch of its own where that kernel does not run.
+struct __attribute__((aligned(32))) RowTile {
+  int32_t n, r0;               // sequence, first row
+  int32_t start, fresh, kv;    // its lengths
+  int32_t lo, hi;              // tiles of keys
+  int32_t unused;
+};
+typedef __attribute__((address_space(4))) const RowTile const_row_tile;
+
 template <typename W, int kThreads>
 __device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part) {
   constexpr int kRows = W::kRows, kKeys = W::kKeys, kOver = W::kOver;
   const int tid = threadIdx.x;
   int64_t* const before = a.sched + 2;
-  int64_t* const which = before + a.max_tiles;
-  int64_t* const starts = which + a.max_tiles;   // row tiles before each sequence
+  RowTile* const which = a.row_tiles;
+  int64_t* const starts = before + a.max_tiles;   // row tiles before each sequence
   int64_t count = 0, sum;
   for (int n0 = 0; n0 < a.N; n0 += kThreads) {
     const int n = n0 + tid;
@@ -639,7 +677,7 @@ __device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part)
       const int32_t rt = i % 2 == 0 ? i / 2 : all - 1 - i / 2, r0 = rt * kRows;
       const Span x = span_of<kKeys>(a, s, r0, max(min(r0 + kRows, s.fresh * a.group) - 1, r0));
       v = x.hi - x.lo + kOver;
-      which[t] = int64_t(lo) << 32 | rt;
+      which[t] = {lo, r0, s.start, s.fresh, s.kv, x.lo, x.hi, 0};
     }
     const int64_t inc = total + block_scan<kThreads>(v, part, sum);
     if (t < count) before[t] = inc - v;
@@ -733,7 +771,8 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     const int32_t t0 = max(in - kNarrowOver, 0), t1 = out - kNarrowOver;
     const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
-    w.start(a, s, hk, lane & 31, rows, lane);
+    w.queries(a, s, hk, lane & 31, rows, lane);
+    w.start(a, s, lane & 31, rows);
 
     constexpr int kSegs = kNarrowKeys / kSeg, kSegLoads = kLoads / kSegs;
     // the pages of the tile to load next are looked up one tile ahead
@@ -977,7 +1016,6 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   if (total == 0) return;
   const Line line(total, a.wide.grid, 1 + P::kOver / 2);
   const int64_t* const before = a.sched + 2;
-  const int64_t* const which = before + a.max_tiles;
   // The unit that holds position `at`: key head, row tile, start.
   auto find = [&](int64_t at, int& head, int& tile, int64_t& start, int64_t& size) {
     head = __builtin_amdgcn_readfirstlane(int(at / per_head));
@@ -1016,56 +1054,94 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     start = pos;
     if (++rt >= count) rt = 0, ++hk;
   }
-  int64_t rest = pos - start;
   Wave<E, D> w;
   lds_u8* const tiles_at = (lds_u8*)buf;
-  while (pos < end) {
-    const int64_t id = which[rt];
-    const int n = __builtin_amdgcn_readfirstlane(int(id >> 32));
-    const Seq s = seq_of(a, n);
-    const int32_t rows = s.fresh * a.group;
-    const int32_t r0 = __builtin_amdgcn_readfirstlane(int(id & 0xFFFFFFFF)) * P::kRows;
-    const Span x = span_of<P::kKeys>(a, s, r0, max(min(r0 + P::kRows, rows) - 1, r0));
-    const int32_t tiles = x.hi - x.lo, size = tiles + P::kOver;
-    const int32_t in = __builtin_amdgcn_readfirstlane(int32_t(rest));   // where this stretch enters the unit and leaves it
-    const int32_t out = __builtin_amdgcn_readfirstlane(int32_t(min(int64_t(size), in + (end - pos))));
-    const int32_t t0 = max(in - P::kOver, 0), t1 = max(out - P::kOver, 0);
-    const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
-    const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
-    const int32_t w0 = r0 + wave * 32;   // this wave's rows
-    const bool busy = w0 < rows;
-    const Span mine = span_of<P::kKeys>(a, s, min(w0, rows - 1), min(w0 + 31, rows - 1));
+  const uint32_t buf_at = uint32_t(uintptr_t(tiles_at));
+  const_row_tile* const list = (const_row_tile*)a.row_tiles;
 
-    // this wave's share of a tile: rows mine_at .., all in one page, looked up one tile ahead
-    constexpr int kMine = P::kKeys / P::kWaves;
-    static_assert(kMine <= kSeg && kSeg % kMine == 0, "one page");
-    const int mine_at = wave * kMine;
-    int32_t page = seg_page(a, row, last_page, (x.lo + t0) * P::kKeys + mine_at);
-    auto load = [&](int32_t t, uint32_t to) {
-      const int32_t j = (x.lo + t) * P::kKeys + mine_at;
-      const int64_t at = seg_offset<E, D>(a, page, hk, j);
-      load_rows<E, D, false, P::kLoads>(a.kc + at, mine_at, to + mine_at * Tile<E, D>::kRowBytes, lane);
-      load_rows<E, D, true, P::kLoads>(a.vc + at, mine_at, to + P::kTileBytes + mine_at * Tile<E, D>::kRowBytes, lane);
-      page = seg_page(a, row, last_page, j + P::kKeys);
-    };
-    uint32_t half = 0;
-    load(t0, uint32_t(uintptr_t(tiles_at)));
-    w.start(a, s, hk, w0 + (lane & 31), rows, lane);
-    for (int32_t t = t0; t < t1; ++t) {
+  // A unit: a row tile of a key head, and the part of its tiles of keys that is this stretch's.
+  struct Unit {
+    Seq s;
+    Span x;
+    int32_t n, hk, rows, r0, in, out, t0, t1;  // in, out: where the stretch enters the unit and leaves it
+  };
+  auto describe = [&](const RowTile& d, int head, int64_t from, int64_t left) {
+    Unit u;
+    u.n = d.n;
+    u.hk = head;
+    u.s = {d.start, d.fresh, d.kv};
+    u.rows = d.fresh * a.group;
+    u.r0 = d.r0;
+    u.x.first = max(d.kv - d.fresh + d.r0 / a.group, -1);
+    u.x.last = max(d.kv - d.fresh + (min(d.r0 + P::kRows, u.rows) - 1) / a.group, -1);
+    u.x.lo = d.lo;
+    u.x.hi = d.hi;
+    u.in = int32_t(from);
+    u.out = int32_t(min(int64_t(d.hi - d.lo + P::kOver), from + left));
+    u.t0 = max(u.in - P::kOver, 0);
+    u.t1 = max(u.out - P::kOver, 0);
+    return u;
+  };
+  auto tile_of = [&](int at) { return *(const RowTile*)(list + at); };
+
+  // this wave's share of a tile of keys: rows mine_at .., all in one page, looked up one tile ahead
+  constexpr int kMine = P::kKeys / P::kWaves;
+  static_assert(kMine <= kSeg && kSeg % kMine == 0, "one page");
+  const int mine_at = wave * kMine;
+  int32_t page;
+  auto look_up = [&](const Unit& u, int32_t t) {
+    page = seg_page(a, (const_i32*)(a.table + int64_t(u.n) * a.width), max((u.s.kv - 1) >> a.lps, 0),
+                    (u.x.lo + t) * P::kKeys + mine_at);
+  };
+  auto load = [&](const Unit& u, int32_t t, uint32_t to) {
+    const int64_t at = seg_offset<E, D>(a, page, u.hk, (u.x.lo + t) * P::kKeys + mine_at);
+    load_rows<E, D, false, P::kLoads>(a.kc + at, mine_at, to + mine_at * Tile<E, D>::kRowBytes, lane);
+    load_rows<E, D, true, P::kLoads>(a.vc + at, mine_at, to + P::kTileBytes + mine_at * Tile<E, D>::kRowBytes, lane);
+  };
+
+  uint32_t half = 0;
+  bool there = false;   // the unit's first tile has been asked for
+  int64_t from = pos - start;
+  for (;;) {
+    const Unit u = describe(tile_of(rt), hk, from, end - pos);
+    if (!there) {
+      look_up(u, u.t0);
+      load(u, u.t0, buf_at + half);
+    }
+    look_up(u, u.t0 + 1);
+    const int32_t w0 = u.r0 + wave * 32;   // this wave's rows
+    w.queries(a, u.s, u.hk, w0 + (lane & 31), u.rows, lane);
+    w.start(a, u.s, w0 + (lane & 31), u.rows);
+    const int64_t after = pos + (u.out - u.in);
+    const bool more = after < end;
+    const bool busy = w0 < u.rows;
+    const int32_t first = max(u.s.kv - u.s.fresh + min(w0, u.rows - 1) / a.group, -1);   // the positions of this wave's rows
+    const int32_t last = max(u.s.kv - u.s.fresh + min(w0 + 31, u.rows - 1) / a.group, -1);
+    for (int32_t t = u.t0; t < u.t1; ++t) {
       wait_loads<0>();
       __syncthreads();   // the tile is there, and every wave is done with the other buffer
-      if (t + 1 < t1) load(t + 1, uint32_t(uintptr_t(tiles_at)) + (half ^ 2 * P::kTileBytes));
-      const int32_t kv0 = (x.lo + t) * P::kKeys;
-      const bool none = !busy || kv0 > mine.last || (a.window > 0 && kv0 + P::kKeys - 1 <= mine.first - a.window);
-      const bool full = kv0 + P::kKeys - 1 <= mine.first && (a.window == 0 || kv0 > mine.last - a.window);
-      if (kv0 + P::kKeys - 1 > x.first || (a.window > 0 && kv0 <= x.last - a.window)) {
+      const uint32_t other = buf_at + (half ^ 2 * P::kTileBytes);
+      if (t + 1 < u.t1) {
+        load(u, t + 1, other);
+        look_up(u, t + 2);
+      } else if (more) {
+        // the next unit's first tile arrives while this unit ends
+        const bool turn = rt + 1 >= count;
+        const Unit v = describe(tile_of(turn ? 0 : rt + 1), turn ? hk + 1 : hk, 0, end - after);
+        look_up(v, v.t0);
+        load(v, v.t0, other);
+      }
+      const int32_t kv0 = (u.x.lo + t) * P::kKeys;
+      const bool none = !busy || kv0 > last || (a.window > 0 && kv0 + P::kKeys - 1 <= first - a.window);
+      const bool full = kv0 + P::kKeys - 1 <= first && (a.window == 0 || kv0 > last - a.window);
+      if (kv0 + P::kKeys - 1 > u.x.first || (a.window > 0 && kv0 <= u.x.last - a.window)) {
         // some row of the workgroup does not see all of it
         lds_u8* const vt = tiles_at + half + P::kTileBytes;
         const bool odd = __any(any_odd<E, P::kTileBytes, P::kThreads>(vt, tid));
         if (lane == 0) odd_waves[wave] = odd;
         __syncthreads();
         int found = 0;
-        for (int v = 0; v < P::kWaves; ++v) found |= odd_waves[v];
+        for (int y = 0; y < P::kWaves; ++y) found |= odd_waves[y];
         if (found) {
           if (!none) w.template mark<P::kKeys>(vt, kv0, lane);
           __syncthreads();
@@ -1080,53 +1156,41 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
       }
       half ^= 2 * P::kTileBytes;
     }
-    __syncthreads();   // before the next unit's loads
 
     const float l_all = w.finish();
-    const bool whole = t0 == 0 && t1 == tiles;
+    const bool whole = u.t0 == 0 && u.t1 == u.x.hi - u.x.lo;
     const int32_t r = w0 + (lane & 31), h = lane >> 5;
     if (whole) {
-      if (r < rows) {
+      if (r < u.rows) {
         const float inv = w.c == -INFINITY ? 0.0f : 1.0f / l_all;
-        const int64_t at = out_row(a, s, hk, r);
-#pragma unroll
-        for (int y = 0; y < D / 32; ++y)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            store4<E>(a.o + (at * D + y * 32 + 8 * k + 4 * h) * sizeof(E), w.o[y][4 * k] * inv, w.o[y][4 * k + 1] * inv,
-                      w.o[y][4 * k + 2] * inv, w.o[y][4 * k + 3] * inv);
+        const int64_t at = out_row(a, u.s, u.hk, r);
+        store_row<E, D>(a.o + at * D * sizeof(E), w.o, inv, h);
         if (a.lse != nullptr && h == 0) a.lse[at] = w.c == -INFINITY ? -INFINITY : (w.c + log2f(l_all)) * kLn2;
       }
     } else {
-      float* const part = a.wide.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(P::kRows);
+      float* const part = a.wide.parts + int64_t(2 * b + (u.t0 == 0 ? 1 : 0)) * part_floats<D>(P::kRows);
       const int q = wave * 32 + (lane & 31);
-      if (r < rows) {
-#pragma unroll
-        for (int y = 0; y < D / 32; ++y)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 f = {w.o[y][4 * k], w.o[y][4 * k + 1], w.o[y][4 * k + 2], w.o[y][4 * k + 3]};
-            *reinterpret_cast<float4*>(part + q * D + y * 32 + 8 * k + 4 * h) = f;
-          }
+      if (r < u.rows) {
+        store_row<float, D>(reinterpret_cast<uint8_t*>(part + q * D), w.o, 1.0f, h);
         if (h == 0) {
           part[P::kRows * D + q] = w.c;
           part[P::kRows * (D + 1) + q] = l_all;
         }
       }
       // the first cut of this unit: the one before is not within it (or has moved to its start)
-      if (tid == 0 && t0 > 0 && line.start(b - 1) <= pos - in + slack) {
-        a.wide.joins[4 * b] = n;
-        a.wide.joins[4 * b + 1] = hk;
-        a.wide.joins[4 * b + 3] = r0;
-        a.wide.joins[4 * b + 2] = int32_t(1 + line.before(pos - in + size - slack) - b);
+      if (tid == 0 && u.t0 > 0 && line.start(b - 1) <= pos - u.in + slack) {
+        const int64_t ends = pos - u.in + (u.x.hi - u.x.lo + P::kOver);
+        a.wide.joins[4 * b] = u.n;
+        a.wide.joins[4 * b + 1] = u.hk;
+        a.wide.joins[4 * b + 3] = u.r0;
+        a.wide.joins[4 * b + 2] = int32_t(1 + line.before(ends - slack) - b);
       }
     }
-    pos += out - in;
-    rest = 0;
-    if (++rt >= count) {
-      rt = 0;
-      ++hk;
-    }
+    if (!more) break;
+    pos = after;
+    from = 0;
+    there = true;
+    if (++rt >= count) rt = 0, ++hk;
   }
 }
 
@@ -1156,7 +1220,7 @@ struct Plan {
   bool narrow, wide;
   int narrow_grid, wide_grid;  // workgroups; of the wide kernel a multiple of 8
   int64_t max_tiles;           // row tiles of the wide kernel at most
-  size_t narrow_joins, narrow_parts, wide_joins, wide_parts, sched, bytes;  // offsets and size of the workspace
+  size_t narrow_joins, narrow_parts, wide_joins, wide_parts, row_tiles, sched, bytes;  // offsets and size of the workspace
 };
 
 template <typename E, int D>
@@ -1187,7 +1251,8 @@ Plan plan_of(const rglru_paged_shape_t& s) {
   if (p.wide) {
     p.max_tiles = ceil_div(s.n_tokens * group, W::kRows) + seqs;
     p.wide_grid = (grid_of(256, p.max_tiles * s.kv_heads, ceil_div(keys, W::kKeys)) + 7) / 8 * 8;
-    p.sched = take(size_t(2 + 2 * p.max_tiles + s.n_seqs) * 8);
+    p.row_tiles = take(size_t(p.max_tiles) * sizeof(RowTile));
+    p.sched = take(size_t(2 + p.max_tiles + s.n_seqs) * 8);
     p.wide_joins = take(size_t(p.wide_grid) * 16);
     p.wide_parts = take(size_t(p.wide_grid) * 2 * part_floats<D>(W::kRows) * 4);
   }
@@ -1209,6 +1274,7 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
   a.wide = {reinterpret_cast<int32_t*>(workspace + p.wide_joins), reinterpret_cast<float*>(workspace + p.wide_parts),
             p.wide_grid};
   a.sched = reinterpret_cast<int64_t*>(workspace + p.sched);
+  a.row_tiles = reinterpret_cast<RowTile*>(workspace + p.row_tiles);
   a.max_tiles = int32_t(p.max_tiles);
   a.least_rows = p.narrow ? kNarrowRows : 0;
   if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid + p.wide), Narrow<E, D>::kThreads, 0, st>>>(a);
