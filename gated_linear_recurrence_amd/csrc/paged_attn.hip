@@ -179,6 +179,7 @@ struct AttnArgs {
   Cuts narrow, wide;
   int64_t q_stride;
   int32_t T, n_pages, N, width, lps, Hq, Hkv, group, window, max_tiles;
+  int32_t own_list;    // the wide kernel's workgroups list the row tiles themselves
   int32_t least_rows;  // the wide kernel's sequences have more rows than this
   float scale2;     // |scale| log2 e (1 for a scale of 0, whose queries are zeroed)
   int32_t q_sign;   // sign of the scale: -1, 0, 1
@@ -539,6 +540,12 @@ __device__ __forceinline__ int64_t out_row(const AttnArgs& a, const Seq& s, int 
   return int64_t(s.start + t) * a.Hq + hk * a.group + (r - t * a.group);
 }
 
+// A value that all lanes share, for the compiler to know.
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32 |
+                 uint32_t(__builtin_amdgcn_readfirstlane(int(v))));
+}
+
 // A partial result: kRows rows of D floats (not normalised), then kRows maxima (log2 units) and kRows sums.
 template <int D>
 constexpr int part_floats(int rows) {
@@ -573,6 +580,10 @@ struct Line {
 // at the end of a unit. What counts is how many bytes are in flight: a
 // wave asks for the next keys (values) as soon as it has read the buffer that they go to.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
+
+// With up to this many sequences in a call that needs the wide kernel, the wide kernel takes those of few rows too: a chunk of
+// 1000 tokens beside 11 single tokens over 2000 keys each takes 60 us so and 63 with both kernels, beside 23 75 and 70.
+constexpr int kFewSeqs = 16;
 
 template <typename E, int D>
 struct Narrow {
@@ -633,7 +644,9 @@ struct Wide {
 
 // The row tiles of all sequences: sched[0] their number, sched[1] the length
 // of one key head's units, then for each tile the length before it, then for each its RowTile.
-// One workgroup writes them: the narrow kernel's last, beside the others' work, or a launch of its own where that kernel does not run.
+// One workgroup writes them: the narrow kernel's last, beside the others' work, or, where that kernel does not run, a
+// launch of its own; up to kOwnTiles of them every workgroup of the wide kernel lists for itself, in LDS, which takes 2 us
+// where the launch takes 6.
 struct __attribute__((aligned(32))) RowTile {
   int32_t n, r0;               // sequence, first row
   int32_t start, fresh, kv;    // its lengths
@@ -643,12 +656,11 @@ struct __attribute__((aligned(32))) RowTile {
 typedef __attribute__((address_space(4))) const RowTile const_row_tile;
 
 template <typename W, int kThreads>
-__device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part) {
+__device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part, int64_t* sched, RowTile* which,
+                                               int64_t* starts) {
   constexpr int kRows = W::kRows, kKeys = W::kKeys, kOver = W::kOver;
   const int tid = threadIdx.x;
-  int64_t* const before = a.sched + 2;
-  RowTile* const which = a.row_tiles;
-  int64_t* const starts = before + a.max_tiles;   // row tiles before each sequence
+  int64_t* const before = sched + 2;   // `starts`: row tiles before each sequence
   int64_t count = 0, sum;
   for (int n0 = 0; n0 < a.N; n0 += kThreads) {
     const int n = n0 + tid;
@@ -684,17 +696,18 @@ __device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part)
     total += sum;
   }
   if (tid == 0) {
-    a.sched[0] = count;
-    a.sched[1] = total;
+    sched[0] = count;
+    sched[1] = total;
   }
 }
 
 constexpr int kSchedThreads = 1024;
+constexpr int kOwnTiles = 256;
 
 template <typename W>
 __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
   __shared__ int64_t part[kSchedThreads / 64];
-  list_row_tiles<W, kSchedThreads>(a, part);
+  list_row_tiles<W, kSchedThreads>(a, part, a.sched, a.row_tiles, a.sched + 2 + a.max_tiles);
 }
 
 // ---- few rows: the kernel ----
@@ -711,7 +724,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int b = blockIdx.x;
   if (b == a.narrow.grid) {
-    list_row_tiles<Wide<E, D>, P::kThreads>(a, scan_part);
+    list_row_tiles<Wide<E, D>, P::kThreads>(a, scan_part, a.sched, a.row_tiles, a.sched + 2 + a.max_tiles);
     return;
   }
 
@@ -942,7 +955,8 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
   const int kRows = wide ? kWideRows : kNarrowRows;
   const int64_t part_size = int64_t(kRows) * (D + 2);
   const int rows = min(kRows, s.fresh * a.group - r0);
-  const bool share = pieces > kShare;   // the sets share a row's pieces
+  // The sets share a row's pieces where there are many and that takes fewer reads in a row than a set per row.
+  const bool share = pieces > kShare && (rows + shares - 1) / shares * kAhead < pieces;
   const int set = tid / kLanes, d = (tid % kLanes) * 4;
   auto write = [&](int q, float c, float l, const float4& acc) {
     const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
@@ -1010,12 +1024,20 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
   const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
-  const int64_t count = a.sched[0], per_head = a.sched[1];
+  // The row tiles, from memory or listed here.
+  __shared__ int64_t own_sched[2 + kOwnTiles], own_starts[kFewSeqs], scan_part[P::kWaves];
+  __shared__ RowTile own_tiles[kOwnTiles];
+  if (a.own_list) {
+    list_row_tiles<P, P::kThreads>(a, scan_part, own_sched, own_tiles, own_starts);
+    __syncthreads();
+  }
+  const int64_t* const sched = a.own_list ? own_sched : a.sched;
+  const int64_t count = uniform(sched[0]), per_head = uniform(sched[1]);
   const int64_t total = per_head * a.Hkv;
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
   if (total == 0) return;
   const Line line(total, a.wide.grid, 1 + P::kOver / 2);
-  const int64_t* const before = a.sched + 2;
+  const int64_t* const before = sched + 2;
   // The unit that holds position `at`: key head, row tile, start.
   auto find = [&](int64_t at, int& head, int& tile, int64_t& start, int64_t& size) {
     head = __builtin_amdgcn_readfirstlane(int(at / per_head));
@@ -1030,8 +1052,9 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
       lo = next;
     }
     tile = __builtin_amdgcn_readfirstlane(int(lo));
-    start = before[tile] + head * per_head;
-    size = (tile + 1 < count ? before[tile + 1] : per_head) - before[tile];
+    const int64_t at_tile = uniform(before[tile]);
+    start = at_tile + head * per_head;
+    size = (tile + 1 < count ? uniform(before[tile + 1]) : per_head) - at_tile;
   };
   // A cut costs a write and a read of a whole output tile, so one that falls near an end of a unit moves there (and one
   // in its fixed part always).
@@ -1082,7 +1105,22 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
     u.t1 = max(u.out - P::kOver, 0);
     return u;
   };
-  auto tile_of = [&](int at) { return *(const RowTile*)(list + at); };
+  auto tile_of = [&](int at) {
+    RowTile d;
+    if (a.own_list) {
+      const RowTile& o = own_tiles[at];
+      d.n = __builtin_amdgcn_readfirstlane(o.n);
+      d.r0 = __builtin_amdgcn_readfirstlane(o.r0);
+      d.start = __builtin_amdgcn_readfirstlane(o.start);
+      d.fresh = __builtin_amdgcn_readfirstlane(o.fresh);
+      d.kv = __builtin_amdgcn_readfirstlane(o.kv);
+      d.lo = __builtin_amdgcn_readfirstlane(o.lo);
+      d.hi = __builtin_amdgcn_readfirstlane(o.hi);
+    } else {
+      d = *(const RowTile*)(list + at);
+    }
+    return d;
+  };
 
   // this wave's share of a tile of keys: rows mine_at .., all in one page, looked up one tile ahead
   constexpr int kMine = P::kKeys / P::kWaves;
@@ -1211,13 +1249,11 @@ int64_t most_rows(const rglru_paged_shape_t& s) {
 }
 
 // A call whose sequences may all have at most kNarrowRows rows runs the narrow
-// kernel alone; any other one the wide kernel, and the narrow kernel before it for the sequences of few
-// rows among more than kFewSeqs. With few sequences the wide kernel takes them all: the launch would cost more
-// than the rows it leaves idle.
-constexpr int kFewSeqs = 4;
-
+// kernel alone (32 sequences of 4096 keys, 32 rows on each of 4 key heads of
+// 128: 60 us, the wide kernel 65); any other one the wide kernel, and before it
+// the narrow kernel for the sequences of few rows among more than kFewSeqs.
 struct Plan {
-  bool narrow, wide;
+  bool narrow, wide, own_list;
   int narrow_grid, wide_grid;  // workgroups; of the wide kernel a multiple of 8
   int64_t max_tiles;           // row tiles of the wide kernel at most
   size_t narrow_joins, narrow_parts, wide_joins, wide_parts, row_tiles, sched, bytes;  // offsets and size of the workspace
@@ -1250,6 +1286,7 @@ Plan plan_of(const rglru_paged_shape_t& s) {
   }
   if (p.wide) {
     p.max_tiles = ceil_div(s.n_tokens * group, W::kRows) + seqs;
+    p.own_list = !p.narrow && p.max_tiles <= kOwnTiles;
     p.wide_grid = (grid_of(256, p.max_tiles * s.kv_heads, ceil_div(keys, W::kKeys)) + 7) / 8 * 8;
     p.row_tiles = take(size_t(p.max_tiles) * sizeof(RowTile));
     p.sched = take(size_t(2 + p.max_tiles + s.n_seqs) * 8);
@@ -1276,10 +1313,11 @@ void launch(const rglru_paged_shape_t& s, AttnArgs a, uint8_t* workspace, hipStr
   a.sched = reinterpret_cast<int64_t*>(workspace + p.sched);
   a.row_tiles = reinterpret_cast<RowTile*>(workspace + p.row_tiles);
   a.max_tiles = int32_t(p.max_tiles);
+  a.own_list = p.own_list;
   a.least_rows = p.narrow ? kNarrowRows : 0;
   if (p.narrow) narrow_kernel<E, D><<<unsigned(p.narrow_grid + p.wide), Narrow<E, D>::kThreads, 0, st>>>(a);
   if (p.wide) {
-    if (!p.narrow) sched_kernel<W><<<1, kSchedThreads, 0, st>>>(a);
+    if (!p.narrow && !p.own_list) sched_kernel<W><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
   // A pass over kPass rows costs the latency of its reads, 2 to 3 us: one pass (rows of few pieces; with many, a row a pass).
