@@ -13,9 +13,9 @@
 // read out of row-major V with the transposing LDS read (4 keys of one column
 // per lane). Scores, maxima, sums and outputs are float32; bf16 weights are
 // rounded to bf16 where they enter the product (what the matrix cores take).
-// The output is rescaled only where the maximum grew by more than 2^8: the
-// weights stay below 2^8 then, which costs float32 and bf16 nothing, and most tiles skip
-// the rescale.
+// The output is rescaled only where the maximum grew by more than 8 (log2):
+// the weights stay below 2^8 then, which costs float32 and bf16 nothing, and
+// most tiles skip the rescale.
 //
 // float32 uses the float32 MFMA with the same lane layouts, eight 2-deep
 // products for one 16-deep one.
@@ -578,7 +578,9 @@ struct Line {
 // the card has some 250. Each wave streams tiles of 32 keys of its own
 // through its own LDS buffers without a barrier; the waves of a workgroup merge
 // at the end of a unit. What counts is how many bytes are in flight: a
-// wave asks for the next keys (values) as soon as it has read the buffer that they go to.
+// wave asks for the next keys (values) as soon as it has read the buffer that
+// they go to. 64 sequences of up to 8192 keys, 8 key heads of 128 in bf16: 0.197
+// ms, 5.5 TB/s; of 32 768 keys: 6.1 TB/s.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
 
 // With up to this many sequences in a call that needs the wide kernel, the wide kernel takes those of few rows too: a chunk of
@@ -624,8 +626,13 @@ __device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) 
 // ---- many rows: chunks of a prompt, and whatever stands beside them in a batch ----
 //
 // Bound by the matrix cores. kRows rows of one (sequence, key head) share
-// every tile of kKeys keys and values, which the waves fetch together into one of two LDS
-// buffers while they work on the other; one barrier a tile.
+// every tile of kKeys keys and values, which the waves fetch together into one
+// of two LDS buffers while they work on the other; one barrier a tile. 2048
+// tokens after 30 011, 32 query and 8 key heads of 128: 0.93 to 0.95 ms, 1.1
+// PFLOP/s, where an 8192^3 library product reaches 1.14 on the same card; the
+// matrix pipes are busy 53 % of the time at the 1.9 GHz that the power allows.
+// Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.56 ms, 0.92
+// PFLOP/s.
 template <typename E, int D>
 struct Wide {
   static constexpr bool kBf16 = sizeof(E) == 2;
@@ -869,7 +876,7 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads)) void narrow_kernel(AttnAr
     __syncthreads();
     const bool whole = t0 == 0 && t1 == tiles;
     float* const part = a.narrow.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
-    // a half of the columns at a time: the merge buffer is one of the two stages
+    // half of the columns at a time, in the buffers of the tiles
 #pragma unroll
     for (int x0 = 0; x0 < D / 32; x0 += (D / 32 + 1) / 2) {
       constexpr int kX = (D / 32 + 1) / 2, kC = kX * 32, kRow = kC + 4;  // 4 floats against bank conflicts

@@ -623,6 +623,13 @@ def _call_on(device, fn, where, *args):
     _lib.check(status, where)
 
 
+def _int32(name, value, least=0):
+    value = int(value)
+    if not least <= value < 1 << 31:
+        raise ValueError(f"{name} is {value}, expected {least} to 2^31 - 1")
+    return value
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -704,10 +711,9 @@ def rglru_page_plan(context_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_
     n_pages = free_pages.numel()
     _need(free_pages, "free_pages", (n_pages,), torch.int32, dev)
     _need(free_count, "free_count", (1,), torch.int32, dev)
-    t = int(n_tokens)
-    shape = _paged_shape(t, n_pages, n, width, int(page_size), 0, 0, 0, 0, int(max_new), 0, 0.0, 0, 0)
-    if t < 0:
-        raise ValueError("n_tokens must not be negative")
+    t = _int32("n_tokens", n_tokens)
+    shape = _paged_shape(t, n_pages, n, width, _int32("page_size", page_size), 0, 0, 0, 0, _int32("max_new", max_new), 0, 0.0,
+                         0, 0)
     outs = (slot_map, positions, kv_lens, held_lens_out, free_count_out, unserved)
     sizes = (t, t, n, n, 1, 1)
     if outs.count(None) == 6:   # pieces of one allocation
@@ -757,8 +763,8 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     int32. Row i of a sequence stands at kv_len - new + i and sees the keys up to its own, with window > 0 the
     last `window` of them. max_new: the most new tokens of a sequence (0: not known; 1 for a decode step picks the
     kernel for few rows). scale defaults to 1 / sqrt(D). workspace: a uint8 device tensor of at least
-    rglru_paged_attn_workspace_bytes bytes, 256-byte aligned (allocated here when None); calls sharing one must
-    not overlap. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
+    rglru_paged_attn_workspace_bytes bytes, 256-byte aligned (allocated here when None; a captured step of many
+    layers should pass one, it is up to 140 MB); calls sharing one must not overlap. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
     lib = _lib.load()
     dev = k_cache.device
     n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)
@@ -773,7 +779,8 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if want_lse or lse is not None:
         lse = _out(lse, "lse", (t, hq), torch.float32, dev)
     sc = (1.0 / float(dim) ** 0.5) if scale is None else float(scale)
-    fields = (t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], int(max_new), int(window), sc, row, 0)
+    fields = (t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], _int32("max_new", max_new),
+              _int32("window", window), sc, row, 0)
     if workspace is None:
         workspace = torch.empty(max(_paged_attn_bytes(*fields), 1), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():

@@ -114,10 +114,12 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *
  * with scores, softmax and sums in float32. A row that sees no key (p < 0, or
  * all its scores -inf) gets o = 0 and lse = -inf. What a row does not see has
- * no influence on it, infinities and NaN included; padding rows of o and lse are left as
- * they were. For bf16 the softmax weights are rounded to bf16 where they enter
- * the product with the values (2^-9 relative each). The same call gives the
- * same bits each time.
+ * no influence on it, infinities and NaN included (at given lengths not on a
+ * bit of it); padding rows of o and lse are left as they were. An infinite
+ * value is taken at its weight, so one whose weight underflows gives NaN. For
+ * bf16 the softmax weights are rounded to bf16 where they enter the product
+ * with the values (2^-8 relative at most). The same call gives the same bits
+ * each time.
  *
  *   cu_seqlens       : [N + 1] int32 as above.       kv_lens : [N] int32, new tokens included.
  *   block_table      : [N, max_pages] int32; pages outside the cache give
@@ -126,8 +128,9 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *   k_cache, v_cache : [n_pages, Hkv, page_size, D] io, 16-byte aligned.
  *   o                : [T, Hq, D] io, dense, 16-byte aligned.
  *   lse              : NULL or [T, Hq] float32.
- *   workspace        : rglru_paged_attn_workspace_bytes(shape) bytes, 256-byte
- *                      aligned; calls that share one must not overlap in time. */
+ *   workspace        : rglru_paged_attn_workspace_bytes(shape) bytes (up to some
+ *                      140 MB, whatever the lengths), 256-byte aligned; calls
+ *                      that share one must not overlap in time. */
 size_t rglru_paged_attn_workspace_bytes(const rglru_paged_shape_t* shape);
 rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* shape, const int32_t* cu_seqlens,
                                     const int32_t* kv_lens, const int32_t* block_table, const void* q,

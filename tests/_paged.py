@@ -78,7 +78,6 @@ class Batch:
         half = HALF[self.dtype]
         o64, lse64 = o.double().cpu().numpy(), lse.double().cpu().numpy()
         assert (o64[self.tokens:] == 7.0).all() and (lse64[self.tokens:] == 7.0).all(), "padding rows were written"
-        worst = 0.0
         for i, m in enumerate(self.new):
             if m == 0:
                 continue
@@ -102,4 +101,3 @@ class Batch:
                 ltol = e + ((seen + 8) * 2.0 ** -23)[:, None] + np.abs(ref_lse) * 2.0 ** -22
                 same = (err <= ltol) | (np.isnan(ref_lse) & np.isnan(lse64[rows])) | (ref_lse == lse64[rows])
             assert same.all(), (i, "lse", np.argwhere(~same)[:5], lse64[rows][~same][:5], ref_lse[~same][:5])
-            worst = max(worst, 0.0)

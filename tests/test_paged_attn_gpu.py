@@ -237,6 +237,47 @@ def test_many_sequences(gpu_lib):
     b.check(*b.call(gpu_lib))
 
 
+@pytest.mark.parametrize("n", [2, 20])
+def test_many_row_tiles(gpu_lib, n):
+    """More row tiles than a workgroup lists for itself, and (20 sequences) than the list's workgroup has threads."""
+    new = [8200 // n - 7 * (i % 3) for i in range(n)]
+    b = Batch([i % 5 for i in range(n)], new, hq=8, hkv=1, dim=64, page=64, seed=n)
+    b.check(*b.call(gpu_lib, window=20), window=20)
+
+
+@pytest.mark.parametrize("n,dim,dtype", [(5, 128, BF), (20, 128, BF), (20, 256, BF), (20, 64, F32), (300, 64, BF)])
+def test_replayed_with_other_lengths(gpu_lib, n, dim, dtype):
+    """One captured call for batches of other shapes: chunks and single tokens change places, sequences come and go,
+    rows turn into padding. Each replay has the bits of an eager call."""
+    rng = np.random.default_rng(n)
+    cap, keys = 700, 160
+    b = Batch([keys] * n, [0] * n, hq=4, hkv=2, dim=dim, page=16, dtype=dtype, pad=cap, seed=n, garbage=0.0)
+    graph = torch.cuda.CUDAGraph()
+    b.call(gpu_lib, max_new=0)
+    torch.cuda.synchronize()
+    o = torch.zeros((cap, 4, dim), dtype=dtype, device="cuda")
+    lse = torch.zeros((cap, 4), device="cuda")
+    args = (b.d_q, b.d_k, b.d_v, b.d_table, b.d_cu, b.d_kv)
+    with torch.cuda.graph(graph):
+        gpu_lib.rglru_paged_attn_fwd(*args, o=o, lse=lse)
+    for step in range(5):
+        new = rng.integers(0, 2, n)
+        if step % 2 == 0:
+            new[rng.integers(0, n)] = int(rng.integers(2, 150))
+        kv = np.maximum(rng.integers(0, keys + 1, n), new)
+        b.new, b.kv, b.cu = new.tolist(), kv.tolist(), np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        b.tokens = int(b.cu[-1])
+        b.d_cu.copy_(torch.from_numpy(b.cu))
+        b.d_kv.copy_(torch.tensor(b.kv, dtype=torch.int32))
+        eager = b.call(gpu_lib, max_new=0)
+        b.check(*eager)
+        o.fill_(7.0), lse.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager[0]) and torch.equal(lse, eager[1])
+
+
 def test_refusals(gpu_lib):
     b = Batch([10], [2], hq=4, hkv=2, dim=64, page=16)
     call = gpu_lib.rglru_paged_attn_fwd

@@ -62,6 +62,9 @@ def test_binding_refuses_before_the_library():
                      (3, good[3].long()), (4, i(0)), (4, good[4].float()), (5, i(3, 3)), (5, good[5].long())):
         with pytest.raises((TypeError, ValueError)):
             glr.rglru_paged_attn_fwd(*good[:n], wrong, *good[n + 1:])
+    for kw in (dict(window=1 << 32), dict(window=-1), dict(max_new=(1 << 32) + 1), dict(max_new=-1)):
+        with pytest.raises(ValueError):
+            glr.rglru_paged_attn_fwd(*good, **kw)
     k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
     for args in ((k, k[:2], kc, kc, i(0, 1, 2)), (k, k.float(), kc, kc, i(0, 1, 2)), (k, k, kc, kc, i(0, 1)), (k[:, :1], k, kc, kc, i(0, 1, 2)),
                  (k.expand(3, 2, 64).transpose(1, 2), k, kc, kc, i(0, 1, 2)), (k[:1].expand(3, 2, 64), k[:1].expand(3, 2, 64), kc, kc, i(0, 1, 2))):
@@ -69,6 +72,7 @@ def test_binding_refuses_before_the_library():
             glr.rglru_paged_kv_write(*args)
     plan = dict(context_lens=i(0), cu_seqlens=i(0, 1), block_table=i(0).view(1, 1), free_pages=i(0), free_count=i(1), n_tokens=1, page_size=16)
     for bad in (dict(context_lens=i(0, 0)), dict(cu_seqlens=i(0)), dict(block_table=i(0)), dict(free_pages=i(0).view(1, 1)),
-                dict(free_count=i(1, 1)), dict(held_lens=i(0, 0)), dict(n_tokens=-1), dict(slot_map=i(0, 0))):
+                dict(free_count=i(1, 1)), dict(held_lens=i(0, 0)), dict(n_tokens=-1), dict(n_tokens=1 << 31), dict(page_size=1 << 32),
+                dict(max_new=(1 << 32) + 1), dict(slot_map=i(0, 0))):
         with pytest.raises((TypeError, ValueError)):
             glr.rglru_page_plan(**{**plan, **bad})
