@@ -630,11 +630,11 @@ __device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) 
 // Bound by the matrix cores. kRows rows of one (sequence, key head) share
 // every tile of kKeys keys and values, which the waves fetch together into one
 // of two LDS buffers while they work on the other; one barrier a tile. 2048
-// tokens after 30 011, 32 query and 8 key heads of 128: 0.93 to 0.95 ms, 1.1
+// tokens after 30 011, 32 query and 8 key heads of 128: 0.92 to 0.99 ms by card, 1.1
 // PFLOP/s, where an 8192^3 library product reaches 1.14 on the same card; the
 // matrix pipes are busy 53 % of the time at the 1.9 GHz that the power allows.
-// Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.56 ms, 0.92
-// PFLOP/s.
+// Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.55 to 0.58 ms,
+// 0.9 PFLOP/s.
 template <typename E, int D>
 struct Wide {
   static constexpr bool kBf16 = sizeof(E) == 2;
