@@ -1375,7 +1375,14 @@ extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, co
       !aligned_to(workspace, 256) || stride * esize % 16 != 0)
     return RGLRU_ERR_MISALIGNED;
   if (s.n_tokens == 0) return RGLRU_OK;
-  if (workspace_bytes < rglru_paged_attn_workspace_bytes(&s)) return RGLRU_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = rglru_paged_attn_workspace_bytes(&s);
+  if (workspace_bytes < need) return RGLRU_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t dense = int64_t(s.q_heads) * s.head_dim, seqs = int64_t(s.n_seqs) * 4;
+  const int64_t cache = s.n_pages * s.page_size * s.kv_heads * s.head_dim * esize;
+  const paged::Bytes outs[] = {{o, s.n_tokens * dense * esize}, {lse, s.n_tokens * s.q_heads * 4}, {workspace, int64_t(need)}};
+  const paged::Bytes ins[] = {{cu_seqlens, seqs + 4}, {kv_lens, seqs},  {block_table, seqs * s.max_pages},
+                              {q, paged::rows_size(s.n_tokens, stride, dense, esize)}, {k_cache, cache}, {v_cache, cache}};
+  if (paged::outputs_overlap(outs, ins)) return RGLRU_ERR_INVALID_ARGUMENT;
   paged::AttnArgs a;
   a.cu = cu_seqlens;
   a.kv_lens = kv_lens;

@@ -260,6 +260,12 @@ extern "C" rglru_status_t rglru_page_plan(const rglru_paged_shape_t* sp, const i
                        slot_map,     free_count_out, positions,  kv_lens,     held_lens_out, unserved};
   for (const void* p : all)
     if (!aligned_to(p, 4)) return RGLRU_ERR_MISALIGNED;
+  const int64_t tokens = s.n_tokens * 4, seqs = int64_t(s.n_seqs) * 4;
+  const paged::Bytes outs[] = {{block_table, seqs * s.max_pages}, {free_pages, s.n_pages * 4}, {free_count_out, 4},
+                               {slot_map, tokens},                {positions, tokens},         {kv_lens, seqs},
+                               {held_lens_out, seqs},             {unserved, 4}};
+  const paged::Bytes ins[] = {{context_lens, seqs}, {held_lens, seqs}, {cu_seqlens, seqs + 4}, {free_count, 4}};
+  if (paged::outputs_overlap(outs, ins)) return RGLRU_ERR_INVALID_ARGUMENT;
   paged::PlanArgs a;
   a.ctx = context_lens;
   a.held = held_lens != nullptr ? held_lens : context_lens;
@@ -312,6 +318,10 @@ extern "C" rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* sp, co
       !aligned_to(slot_map, 4) || stride * esize % 16 != 0)
     return RGLRU_ERR_MISALIGNED;
   if (pieces == 0) return RGLRU_OK;
+  const int64_t cache = s.n_pages * s.page_size * dense * esize, rows = paged::rows_size(s.n_tokens, stride, dense, esize);
+  const paged::Bytes outs[] = {{k_cache, cache}, {v_cache, cache}};
+  const paged::Bytes ins[] = {{k, rows}, {v, rows}, {slot_map, s.n_tokens * 4}};
+  if (paged::outputs_overlap(outs, ins)) return RGLRU_ERR_INVALID_ARGUMENT;
   paged::WriteArgs a;
   a.k = static_cast<const uint4*>(k);
   a.v = static_cast<const uint4*>(v);

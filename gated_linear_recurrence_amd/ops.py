@@ -615,6 +615,8 @@ def _paged_attn_bytes(*fields) -> int:
 
 def _call_on(device, fn, where, *args):
     """Calls a library function on the current stream of `device` (made current for it where another one is)."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: tensors are on {device}, expected a GPU")
     if device.index is None or device.index == torch.cuda.current_device():
         status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
     else:

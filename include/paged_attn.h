@@ -35,7 +35,9 @@ extern "C" {
  * io_dtype an rglru_io_t; max_new, window >= 0; a finite scale; strides 0 or
  * at least the dense row. Within them, a head_dim other than 64, 128 or 256
  * is RGLRU_ERR_UNSUPPORTED, and a stride that is not a multiple of 16 bytes
- * RGLRU_ERR_MISALIGNED. */
+ * RGLRU_ERR_MISALIGNED. An output (what is updated in place and the workspace
+ * too) that overlaps another one or an input is RGLRU_ERR_INVALID_ARGUMENT;
+ * strided rows count from the first one's start to the last one's end. */
 typedef struct {
   int64_t n_tokens;   /* T: rows of the packed batch (a capacity: rows from cu_seqlens[n_seqs] on are padding) */
   int64_t n_pages;    /* pages of the cache */
@@ -82,8 +84,7 @@ typedef struct {
  *   held_lens_out: [N] int32 out: context + new, or held_lens as it was if not served.
  *   unserved     : [1] int32 out: sequences that were not served.
  *
- * No output may overlap an input (free_count_out apart from free_count too);
- * all pointers 4-byte aligned. Reads the shape's n_tokens, n_pages, n_seqs,
+ * All pointers 4-byte aligned. Reads the shape's n_tokens, n_pages, n_seqs,
  * max_pages, page_size and max_new. Lengths outside what is said above give
  * unspecified results, every access staying in bounds. */
 rglru_status_t rglru_page_plan(const rglru_paged_shape_t* shape, const int32_t* context_lens,

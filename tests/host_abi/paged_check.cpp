@@ -149,6 +149,50 @@ int main() {
   EXPECT(plan(&s, nullptr) == RGLRU_ERR_INVALID_ARGUMENT && plan(&s, fake<int32_t>(0x200000), nullptr) == RGLRU_ERR_INVALID_ARGUMENT);
   EXPECT(plan(&s, fake<int32_t>(0x200002)) == RGLRU_ERR_MISALIGNED);
 
+  // outputs that overlap an input or each other, by a whole array or by its last bytes; every array has a place of its own otherwise
+  s = shape();
+  {
+    const size_t need = rglru_paged_attn_workspace_bytes(&s);
+    const int64_t o_size = s.n_tokens * s.q_heads * s.head_dim * 2, cache = s.n_pages * s.page_size * s.kv_heads * s.head_dim * 2;
+    auto at = [](int i) { return (uintptr_t(i) + 1) << 32; };
+    auto run = [&](int moved, uintptr_t to) {
+      uintptr_t p[9];
+      for (int i = 0; i < 9; ++i) p[i] = i == moved ? to : at(i);
+      return rglru_paged_attn_fwd(&s, fake<int32_t>(p[0]), fake<int32_t>(p[1]), fake<int32_t>(p[2]), fake<void>(p[3]), fake<void>(p[4]),
+                                  fake<void>(p[5]), fake<void>(p[6]), fake<float>(p[7]), fake<void>(p[8]), need, nullptr);
+    };
+    for (int in = 0; in < 6; ++in)
+      for (int out = 6; out < 9; ++out) EXPECT(run(out, at(in)) == RGLRU_ERR_INVALID_ARGUMENT);
+    EXPECT(run(7, at(6)) == RGLRU_ERR_INVALID_ARGUMENT && run(8, at(7)) == RGLRU_ERR_INVALID_ARGUMENT);
+    EXPECT(run(3, at(6) + o_size - 16) == RGLRU_ERR_INVALID_ARGUMENT && run(6, at(5) + cache - 16) == RGLRU_ERR_INVALID_ARGUMENT);
+    EXPECT(run(4, at(6) + 16 - cache) == RGLRU_ERR_INVALID_ARGUMENT);
+    auto put = [&](int moved, uintptr_t to) {
+      uintptr_t p[5];
+      for (int i = 0; i < 5; ++i) p[i] = i == moved ? to : at(i);
+      return rglru_paged_kv_write(&s, fake<void>(p[0]), fake<void>(p[1]), fake<void>(p[2]), fake<void>(p[3]), fake<int32_t>(p[4]), nullptr);
+    };
+    EXPECT(put(3, at(2)) == RGLRU_ERR_INVALID_ARGUMENT && put(3, at(2) + cache - 16) == RGLRU_ERR_INVALID_ARGUMENT);
+    for (int in : {0, 1, 4}) EXPECT(put(2, at(in)) == RGLRU_ERR_INVALID_ARGUMENT && put(in, at(3) + 16) == RGLRU_ERR_INVALID_ARGUMENT);
+    s.n_tokens = (int64_t(1) << 31) - 1;   // the longest span there is
+    s.kv_stride = (int64_t(1) << 31) - 8;
+    s.kv_heads = 1;
+    s.head_dim = 16;
+    s.io_dtype = RGLRU_IO_F32;
+    EXPECT(put(2, at(0)) == RGLRU_ERR_INVALID_ARGUMENT);
+    s = shape();
+    auto lay = [&](int moved, uintptr_t to) {
+      uintptr_t p[12];
+      for (int i = 0; i < 12; ++i) p[i] = i == moved ? to : at(i);
+      return rglru_page_plan(&s, fake<int32_t>(p[0]), fake<int32_t>(p[1]), fake<int32_t>(p[2]), fake<int32_t>(p[4]), fake<int32_t>(p[5]),
+                             fake<int32_t>(p[3]), fake<int32_t>(p[6]), fake<int32_t>(p[7]), fake<int32_t>(p[8]), fake<int32_t>(p[9]),
+                             fake<int32_t>(p[10]), fake<int32_t>(p[11]), nullptr);
+    };
+    for (int out = 4; out < 12; ++out)
+      for (int other = 0; other < 12; ++other)
+        if (other != out) EXPECT(lay(out, at(other)) == RGLRU_ERR_INVALID_ARGUMENT);
+    EXPECT(lay(9, at(0) + 8) == RGLRU_ERR_INVALID_ARGUMENT && lay(9, at(2) + 12) == RGLRU_ERR_INVALID_ARGUMENT);
+  }
+
   // nothing to do is not an error, and needs no pointers
   s = shape();
   s.n_tokens = 0;

@@ -76,3 +76,16 @@ def test_binding_refuses_before_the_library():
                 dict(max_new=(1 << 32) + 1), dict(slot_map=i(0, 0))):
         with pytest.raises((TypeError, ValueError)):
             glr.rglru_page_plan(**{**plan, **bad})
+
+
+def test_valid_arguments_on_the_cpu_are_refused():
+    """A call that is right in everything but where its tensors live raises ValueError, with no GPU touched."""
+    kc, vc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32)  # noqa: E731
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        glr.rglru_paged_attn_fwd(k, kc, vc, i(0, 1).view(1, 2), i(0, 3), i(3))
+    with pytest.raises(ValueError, match="expected a GPU"):
+        glr.rglru_paged_kv_write(k, k + 1, kc, vc, i(0, 1, 2))
+    with pytest.raises(ValueError, match="expected a GPU"):
+        glr.rglru_page_plan(i(0), i(0, 1), i(0).view(1, 1), i(0), i(1), n_tokens=1, page_size=16)
