@@ -252,6 +252,21 @@ __device__ __forceinline__ void load_rows(const uint8_t* base, int r, uint32_t t
   }
 }
 
+// The same for 8 rows of slice `c` of a tile that lies in slices of kSlice columns: rows r .. r + 7, kept kRowBytes apart.
+template <typename E, int D, int kSlice, bool kValues>
+__device__ __forceinline__ void load_slice(const uint8_t* base, int c, int r, uint32_t to, int lane) {
+  using L = Tile<E, kSlice>;
+  const int x = lane / L::kCols, col = lane % L::kCols;
+  const int lane_swz = kValues ? L::swz_v(x) : L::swz_k(x);
+#pragma unroll
+  for (int i = 0; i < kSeg / L::kLoadRows; ++i) {
+    const int row = r + i * L::kLoadRows;
+    const int load_swz = kValues ? L::swz_v(row) : L::swz_k(row);
+    const uint32_t off = uint32_t((((col ^ lane_swz) * 16) ^ (load_swz * 16)) + x * Tile<E, D>::kRowBytes);
+    load_lds<0>(to + i * 1024, off, base + c * L::kRowBytes + i * L::kLoadRows * Tile<E, D>::kRowBytes);
+  }
+}
+
 // Waits until at most kMost vector memory operations of this wave are in flight (63 where that is more than can be said).
 template <int kMost>
 __device__ __forceinline__ void wait_loads() {
@@ -273,10 +288,19 @@ __device__ __forceinline__ void wait_reads() {
   asm volatile("" ::: "memory");
 }
 
-// 32 rows of one wave.
-template <typename E, int D>
+struct Nothing {
+  __device__ __forceinline__ void operator()(int) const {}
+};
+
+// 32 rows of one wave. A tile may lie in LDS as slices of kSlice columns, each laid out like a tile of that width, so
+// that one slice is fetched into while others are read.
+template <typename E, int D, int kSlice = D>
 struct Wave {
-  using L = Tile<E, D>;
+  using L = Tile<E, kSlice>;
+  static constexpr int kSlices = D / kSlice;
+  static constexpr int kHeld = kSlices > 1 ? D / 32 : D / 16;  // operands of queries in registers; the others in LDS, at `rest`
+  static constexpr int kRestBytes = (D / 16 - kHeld) * 64 * int(sizeof(Frag<E>));
+  lds_u8* rest;
   Frag<E> q[D / 16];
   f32x16 o[D / 32];
   float m, c, l;     // running maximum of the scores, the same times scale2 (log2 units), sum of the weights (this half-wave's keys)
@@ -309,6 +333,21 @@ struct Wave {
     lo = a.window > 0 ? max(hi - a.window + 1, 0) : 0;
   }
 
+  // Operand kHeld + i of the queries, kept in LDS in pieces of 16 bytes a lane.
+  __device__ __forceinline__ void put_query(int i, int lane) {
+    auto* const to = (__attribute__((address_space(3))) u32x4*)(rest + i * 64 * int(sizeof(Frag<E>)));
+#pragma unroll
+    for (int j = 0; j < int(sizeof(Frag<E>)) / 16; ++j)
+      to[j * 64 + lane] = reinterpret_cast<const u32x4*>(&q[kHeld + i])[j];
+  }
+  __device__ __forceinline__ Frag<E> get_query(int i, int lane) const {
+    Frag<E> f;
+    const auto* const from = (const __attribute__((address_space(3))) u32x4*)(rest + i * 64 * int(sizeof(Frag<E>)));
+#pragma unroll
+    for (int j = 0; j < int(sizeof(Frag<E>)) / 16; ++j) reinterpret_cast<u32x4*>(&f)[j] = from[j * 64 + lane];
+    return f;
+  }
+
   // The sum over both half-waves. A row whose scores are all NaN has no maximum: it gets one, so that it is not taken
   // for a row that sees nothing.
   __device__ __forceinline__ float finish() {
@@ -317,23 +356,27 @@ struct Wave {
     return sum;
   }
 
-  // Weights of BN keys from kv0 on; `full`: every row of the wave sees them all. `done` is called when the keys have
-  // been read.
-  template <int BN, typename Done>
+  // Weights of BN keys from kv0 on; `full`: every row of the wave sees them all. done(c) is called when the reads of
+  // slice c have been issued, and its last product; of several slices ready(c) before its first read.
+  template <int BN, typename Done, typename Ready = Nothing>
   __device__ __forceinline__ void scores(const AttnArgs& a, const lds_u8* kt, int32_t kv0, bool full, int lane,
-                                         Frag<E>* p, Done done) {
+                                         Frag<E>* p, Done done, Ready ready = {}) {
     const int h = lane >> 5;
     f32x16 s[BN / 32];
     {
       // product i: keys of subtile i / (D / 16), elements 16 (i % (D / 16)) on; operands are read kAhead products early
       constexpr int kSteps = D / 16, kAll = BN / 32 * kSteps, kAhead = sizeof(E) == 2 ? 4 : 2;
+      constexpr int kOne = kSteps / kSlices;
+      static_assert(kSlices == 1 || (BN == 32 && kAhead < kOne), "a slice's products follow each other");
       const int r = lane & 31;
       int at = r * L::kRowBytes + (sizeof(E) == 2 ? (h ^ L::swz_k(r)) * 16 : ((2 * h) ^ L::swz_k(r)) * 16);
       fresh_value(at);
-      Frag<E> k[kAhead];
+      Frag<E> k[kAhead], z[kAhead];
       auto fetch = [&](int i) {
-        const int b = i / kSteps, x = i % kSteps;
-        const lds_u8* p = kt + b * 32 * L::kRowBytes;
+        const int b = i / kSteps, x = i % kOne;
+        const lds_u8* p = kt + (b + i % kSteps / kOne) * 32 * L::kRowBytes;
+        if (kSlices > 1 && x == 0) ready(i / kOne);
+        if (i % kSteps >= kHeld) z[i % kAhead] = get_query(i % kSteps - kHeld, lane);
         if constexpr (sizeof(E) == 2) {
           k[i % kAhead].w = *(const __attribute__((address_space(3))) u32x4*)(p + (at ^ (x * 32)));
         } else {
@@ -349,12 +392,13 @@ struct Wave {
 #pragma unroll
       for (int i = 0; i < kAll; ++i) {
         const int b = i / kSteps, x = i % kSteps;
-        s[b] = mma(k[i % kAhead], q[x], s[b]);
+        s[b] = mma(k[i % kAhead], x < kHeld ? q[x] : z[i % kAhead], s[b]);
+        if (kSlices > 1 && i % kOne == kOne - 1) done(i / kOne);
         if (i + kAhead < kAll) fetch(i + kAhead);
         order();
       }
     }
-    done();
+    if (kSlices == 1) done(0);
     if (!full) {
 #pragma unroll
       for (int b = 0; b < BN / 32; ++b)
@@ -399,19 +443,27 @@ struct Wave {
     l += sum;
   }
 
-  // Adds BN weighted values to the output.
-  template <int BN>
-  __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane) {
-    constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = sizeof(E) == 2 ? 4 : 2;
+  // Adds BN weighted values to the output; ready(c) and done(c) as above, of several slices.
+  template <int BN, typename Ready = Nothing, typename Done = Nothing>
+  __device__ __forceinline__ void values(const lds_u8* vt, const Frag<E>* p, int lane, Ready ready = {}, Done done = {}) {
+    constexpr int kSteps = BN / 16, kAll = D / 32 * kSteps, kAhead = sizeof(E) == 2 ? 4 : 2, kOne = kAll / kSlices;
+    static_assert(kSlices == 1 || kAhead < kOne, "a slice's products follow each other");
     int start = value_at(lane);
     fresh_value(start);
     Frag<E> v[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) v[i] = value_frag(vt, i / kSteps, i % kSteps, start);
+    for (int i = 0; i < kAhead; ++i) {
+      if (kSlices > 1 && i == 0) ready(0);
+      v[i] = value_frag<BN>(vt, i / kSteps, i % kSteps, start);
+    }
 #pragma unroll
     for (int i = 0; i < kAll; ++i) {
       o[i / kSteps] = mma(v[i % kAhead], p[i % kSteps], o[i / kSteps]);
-      if (i + kAhead < kAll) v[i % kAhead] = value_frag(vt, (i + kAhead) / kSteps, (i + kAhead) % kSteps, start);
+      if (kSlices > 1 && i % kOne == kOne - 1) done(i / kOne);
+      if (i + kAhead < kAll) {
+        if (kSlices > 1 && (i + kAhead) % kOne == 0) ready((i + kAhead) / kOne);
+        v[i % kAhead] = value_frag<BN>(vt, (i + kAhead) / kSteps, (i + kAhead) % kSteps, start);
+      }
       order();
     }
   }
@@ -431,9 +483,11 @@ struct Wave {
 
   // The operand of columns 32 x .. and keys 16 y .. of a tile. 32 columns are 4 (8) pieces of a row, which the swizzle
   // takes to others of the row's pieces: an XOR.
+  template <int BN>
   __device__ __forceinline__ Frag<E> value_frag(const lds_u8* vt, int x, int y, int start) const {
     Frag<E> v;
-    const int at = (start ^ (x * 32 * int(sizeof(E)))) + y * 16 * L::kRowBytes;
+    constexpr int kCols = kSlice / 32;
+    const int at = (start ^ (x % kCols * 32 * int(sizeof(E)))) + (x / kCols * BN + y * 16) * L::kRowBytes;
     if constexpr (sizeof(E) == 2) {
       const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + at));
       const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -450,8 +504,9 @@ struct Wave {
 
   // Marks what values that are not finite do to this wave's rows: a row that sees a +inf or a NaN gets +inf in its
   // column, one that sees a -inf or a NaN gets -inf (so NaN gives NaN). Products of 0/1 operands, which are finite.
+  // The columns of slice c.
   template <int BN>
-  __device__ __forceinline__ void mark(const lds_u8* vt, int32_t kv0, int lane) {
+  __device__ __forceinline__ void mark(const lds_u8* vt, int32_t kv0, int lane, int c) {
     Frag<E> see[BN / 16];
 #pragma unroll
     for (int y = 0; y < BN / 16; ++y) {
@@ -464,12 +519,12 @@ struct Wave {
       see[y] = pack(one, E{});
     }
 #pragma unroll
-    for (int x = 0; x < D / 32; ++x)
+    for (int x = c * (kSlice / 32); x < (c + 1) * (kSlice / 32); ++x)
 #pragma unroll 1
       for (uint32_t sign = 0; sign < 2; ++sign) {
         f32x16 sum = 0.0f;
 #pragma unroll
-        for (int y = 0; y < BN / 16; ++y) sum = mma(marks(value_frag(vt, x, y, value_at(lane)), sign), see[y], sum);
+        for (int y = 0; y < BN / 16; ++y) sum = mma(marks(value_frag<BN>(vt, x, y, value_at(lane)), sign), see[y], sum);
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[x][r] += sum[r] > 0.0f ? (sign ? -INFINITY : INFINITY) : 0.0f;
       }
@@ -591,13 +646,18 @@ template <typename E, int D>
 struct Narrow {
   static constexpr int kTileBytes = kNarrowKeys * D * int(sizeof(E));
   // 128 KB of LDS per CU, four waves in a workgroup. Up to 8 KB a tile each wave has two buffers of keys and two of
-  // values (and there are two workgroups at 4 KB), at 16 KB one of each, at 32 KB one for both in turn. kGroups also tells
+  // values (and there are two workgroups at 4 KB), at 16 KB one of each, at 32 KB one for both. kGroups also tells
   // the compiler how many waves share a SIMD: with two it keeps the output out of the accumulation registers, which it
   // copies to and fro otherwise (D = 64: 22.4 -> 21 us for 16 sequences of 2000 keys).
   static constexpr int kWaves = 4;
   static constexpr int kBuffers = kTileBytes <= 8192 ? 4 : 32768 / kTileBytes;
   static constexpr int kGroups = kTileBytes == 4096 ? 2 : 1;
   static constexpr int kThreads = kWaves * 64;
+  // The one buffer holds four slices of columns, each loaded anew as soon as it is read: those of the values take the
+  // place of those of the keys and the other way round. Half of the queries lie in LDS, as the registers would not hold
+  // them and the output (float32, D = 256, 64 sequences of 8000 keys, 2 key heads: whole tiles in turn 3.9 TB/s, slices
+  // 4.4, with half of the queries in LDS 5.1).
+  static constexpr int kSlice = kBuffers == 1 ? D / 4 : D;
 };
 
 template <int kThreads>
@@ -724,7 +784,8 @@ template <typename E, int D>
 __global__ __launch_bounds__((Narrow<E, D>::kThreads), (Narrow<E, D>::kGroups)) void narrow_kernel(AttnArgs a) {
   using P = Narrow<E, D>;
   constexpr int kLoads = P::kTileBytes / 1024;
-  __shared__ __align__(1024) unsigned char buf[P::kWaves * P::kBuffers * P::kTileBytes];
+  using W = Wave<E, D, P::kSlice>;
+  __shared__ __align__(1024) unsigned char buf[P::kWaves * P::kBuffers * P::kTileBytes + W::kRestBytes];
   __shared__ int64_t scan_part[P::kWaves];
   __shared__ Seq found;
   __shared__ int32_t found_seq;
@@ -776,7 +837,8 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads), (Narrow<E, D>::kGroups)) 
   int64_t rest = found_rest;   // position within the sequence's units
   Seq s = {__builtin_amdgcn_readfirstlane(found.start), __builtin_amdgcn_readfirstlane(found.fresh),
            __builtin_amdgcn_readfirstlane(found.kv)};
-  Wave<E, D> w;
+  W w;
+  w.rest = (lds_u8*)buf + P::kWaves * P::kBuffers * P::kTileBytes;
   lds_u8* const mine = (lds_u8*)buf + wave * P::kBuffers * P::kTileBytes;
   while (pos < end && n < a.N) {
     const int32_t rows = int64_t(s.fresh) * a.group > kNarrowRows ? 0 : s.fresh * a.group;
@@ -795,6 +857,12 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads), (Narrow<E, D>::kGroups)) 
     const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
     w.queries(a, s, hk, lane & 31, rows, lane);
     w.start(a, s, lane & 31, rows);
+    if constexpr (W::kRestBytes > 0) {
+#pragma unroll
+      for (int i = 0; i < D / 16 - W::kHeld; ++i)
+        if (i % P::kWaves == wave) w.put_query(i, lane);
+      __syncthreads();
+    }
 
     constexpr int kSegs = kNarrowKeys / kSeg, kSegLoads = kLoads / kSegs;
     // the pages of the tile to load next are looked up one tile ahead
@@ -805,65 +873,130 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads), (Narrow<E, D>::kGroups)) 
 #pragma unroll
       for (int i = 0; i < kSegs; ++i) pages[i] = seg_page(a, row, last_page, kv0 + i * kSeg);
     };
-    auto load_keys = [&](int32_t t, uint32_t to) {
+    auto locate = [&](int32_t t) {
       const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kNarrowKeys);
 #pragma unroll
-      for (int i = 0; i < kSegs; ++i) {
-        at[i] = seg_offset<E, D>(a, pages[i], hk, kv0 + i * kSeg);
-        load_rows<E, D, false, kSegLoads>(a.kc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
-      }
-    };
-    auto load_values = [&](uint32_t to) {
-#pragma unroll
-      for (int i = 0; i < kSegs; ++i)
-        load_rows<E, D, true, kSegLoads>(a.vc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
+      for (int i = 0; i < kSegs; ++i) at[i] = seg_offset<E, D>(a, pages[i], hk, kv0 + i * kSeg);
     };
     // mine: the buffers of keys, then those of values
-    constexpr int kW = P::kWaves, kTwo = P::kBuffers == 4, kShared = P::kBuffers == 1;
-    constexpr int kValues = kShared ? 0 : P::kBuffers / 2 * P::kTileBytes;
-    const uint32_t keys_at = uint32_t(uintptr_t(mine)), values_at = keys_at + kValues;
-    uint32_t half = 0;
+    constexpr int kW = P::kWaves, kTwo = P::kBuffers == 4;
+    const uint32_t keys_at = uint32_t(uintptr_t(mine));
     look_up(t0 + wave);
     wait_loads<0>();   // no store of the unit before is counted below
+    if constexpr (P::kBuffers > 1) {
+      auto load_keys = [&](int32_t t, uint32_t to) {
+        locate(t);
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i)
+          load_rows<E, D, false, kSegLoads>(a.kc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
+      };
+      auto load_values = [&](uint32_t to) {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i)
+          load_rows<E, D, true, kSegLoads>(a.vc + at[i], i * kSeg, to + i * kSegLoads * 1024, lane);
+      };
+      constexpr int kValues = P::kBuffers / 2 * P::kTileBytes;
+      const uint32_t values_at = keys_at + kValues;
+      uint32_t half = 0;
 #pragma unroll 1
-    for (int i = 0; i < 1 + kTwo; ++i)
-      if (t0 + wave + i * kW < t1) {
-        load_keys(t0 + wave + i * kW, keys_at + i * P::kTileBytes);
-        if (!kShared) load_values(values_at + i * P::kTileBytes);
-        look_up(t0 + wave + (i + 1) * kW);
+      for (int i = 0; i < 1 + kTwo; ++i)
+        if (t0 + wave + i * kW < t1) {
+          load_keys(t0 + wave + i * kW, keys_at + i * P::kTileBytes);
+          load_values(values_at + i * P::kTileBytes);
+          look_up(t0 + wave + (i + 1) * kW);
+        }
+      for (int32_t t = t0 + wave; t < t1; t += kW) {
+        const bool next = t + kW < t1;                // a further tile
+        const bool after = t + (1 + kTwo) * kW < t1;  // and one for the buffers that this tile leaves
+        const int32_t kv0 = (x.lo + t) * kNarrowKeys;
+        const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
+        Frag<E> p[kNarrowKeys / 16];
+        // behind these keys are in flight: these values and, of two buffers, the next tile
+        if (kTwo && next) wait_loads<3 * kLoads>();
+        else wait_loads<kLoads>();
+        w.template scores<kNarrowKeys>(a, mine + half, kv0, full, lane, p, [&](int) {
+          if (after) {
+            wait_reads();
+            load_keys(t + (1 + kTwo) * kW, keys_at + half);
+          }
+        });
+        // behind these values: the keys just asked for and, of two buffers, the next tile
+        if (kTwo && after) wait_loads<3 * kLoads>();
+        else if (kTwo && next) wait_loads<2 * kLoads>();
+        else if (!kTwo && after) wait_loads<kLoads>();
+        else wait_loads<0>();
+        lds_u8* const vt = mine + kValues + half;
+        if (!full && __any(any_odd<E, P::kTileBytes, 64>(vt, lane))) {
+          w.template mark<kNarrowKeys>(vt, kv0, lane, 0);
+          clean<E, P::kTileBytes, 64>(vt, lane);
+        }
+        w.template values<kNarrowKeys>(vt, p, lane);
+        if (after) {
+          wait_reads();
+          load_values(values_at + half);
+          look_up(t + (2 + kTwo) * kW);
+        }
+        if (kTwo) half ^= P::kTileBytes;
       }
-    for (int32_t t = t0 + wave; t < t1; t += kW) {
-      const bool next = t + kW < t1;                // a further tile
-      const bool after = t + (1 + kTwo) * kW < t1;  // and one for the buffers that this tile leaves
-      const int32_t kv0 = (x.lo + t) * kNarrowKeys;
-      const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
-      Frag<E> p[kNarrowKeys / 16];
-      // behind these keys are in flight: these values and, of two buffers, the next tile
-      if (kTwo && next) wait_loads<3 * kLoads>();
-      else wait_loads<kShared ? 0 : kLoads>();
-      w.template scores<kNarrowKeys>(a, mine + half, kv0, full, lane, p, [&] {
-        if (kShared || after) wait_reads();
-        if (kShared) load_values(values_at);
-        else if (after) load_keys(t + (1 + kTwo) * kW, keys_at + half);
-      });
-      // behind these values: the keys just asked for and, of two buffers, the next tile
-      if (kTwo && after) wait_loads<3 * kLoads>();
-      else if (kTwo && next) wait_loads<2 * kLoads>();
-      else if (!kTwo && !kShared && after) wait_loads<kLoads>();
-      else wait_loads<0>();
-      lds_u8* const vt = mine + kValues + half;
-      if (!full && __any(any_odd<E, P::kTileBytes, 64>(vt, lane))) {
-        w.template mark<kNarrowKeys>(vt, kv0, lane);
-        clean<E, P::kTileBytes, 64>(vt, lane);
+    } else {
+      constexpr int kSlices = D / P::kSlice, kSliceLoads = kLoads / kSlices, kSliceBytes = P::kTileBytes / kSlices;
+      static_assert(kSlices == 4, "the waits below");
+      auto load_keys = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i)
+          load_slice<E, D, P::kSlice, false>(a.kc + at[i], c, i * kSeg, keys_at + c * kSliceBytes + i * (kSliceBytes / kSegs), lane);
+      };
+      auto load_values = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kSegs; ++i)
+          load_slice<E, D, P::kSlice, true>(a.vc + at[i], c, i * kSeg, keys_at + c * kSliceBytes + i * (kSliceBytes / kSegs), lane);
+      };
+      if (t0 + wave < t1) {
+        locate(t0 + wave);
+#pragma unroll
+        for (int c = 0; c < kSlices; ++c) load_keys(c);
+        look_up(t0 + wave + kW);
       }
-      w.template values<kNarrowKeys>(vt, p, lane);
-      if (after) {
-        wait_reads();
-        if (kShared) load_keys(t + kW, keys_at);
-        else load_values(values_at + half);
-        look_up(t + (2 + kTwo) * kW);
+      for (int32_t t = t0 + wave; t < t1; t += kW) {
+        const bool next = t + kW < t1;
+        const int32_t kv0 = (x.lo + t) * kNarrowKeys;
+        const bool full = kv0 + kNarrowKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
+        Frag<E> p[kNarrowKeys / 16];
+        // A slice is waited for when the one before it has not quite been read: behind it are in flight the later ones
+        // and those that took the place of the earlier ones but for the last, two in all; behind the first, three.
+        w.template scores<kNarrowKeys>(
+            a, mine, kv0, full, lane, p,
+            [&](int c) {
+              wait_reads();
+              load_values(c);
+            },
+            [&](int c) {
+              if (c == 0) wait_loads<3 * kSliceLoads>();
+              else wait_loads<2 * kSliceLoads>();
+            });
+        if (next) {
+          locate(t + kW);
+          look_up(t + 2 * kW);
+        }
+        w.template values<kNarrowKeys>(
+            mine, p, lane,
+            [&](int c) {
+              if (c == 0) wait_loads<3 * kSliceLoads>();
+              else if (c == 1 || next) wait_loads<2 * kSliceLoads>();
+              else if (c == 2) wait_loads<kSliceLoads>();
+              else wait_loads<0>();
+              lds_u8* const vt = mine + c * kSliceBytes;
+              if (!full && __any(any_odd<E, kSliceBytes, 64>(vt, lane))) {
+                w.template mark<kNarrowKeys>(mine, kv0, lane, c);
+                clean<E, kSliceBytes, 64>(vt, lane);
+              }
+            },
+            [&](int c) {
+              if (!next) return;
+              wait_reads();
+              load_keys(c);
+            });
       }
-      if (kTwo) half ^= P::kTileBytes;
     }
 
     // The waves merge: maxima and sums first, then every thread sums some columns over the waves.
@@ -1191,7 +1324,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
         int found = 0;
         for (int y = 0; y < P::kWaves; ++y) found |= odd_waves[y];
         if (found) {
-          if (!none) w.template mark<P::kKeys>(vt, kv0, lane);
+          if (!none) w.template mark<P::kKeys>(vt, kv0, lane, 0);
           __syncthreads();
           clean<E, P::kTileBytes, P::kThreads>(vt, tid);
           __syncthreads();
@@ -1199,7 +1332,7 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
       }
       if (!none) {
         Frag<E> p[P::kKeys / 16];
-        w.template scores<P::kKeys>(a, tiles_at + half, kv0, full, lane, p, [] {});
+        w.template scores<P::kKeys>(a, tiles_at + half, kv0, full, lane, p, Nothing{});
         w.template values<P::kKeys>(tiles_at + half + P::kTileBytes, p, lane);
       }
       half ^= 2 * P::kTileBytes;
