@@ -109,6 +109,31 @@ def test_infinite_values_that_are_seen(gpu_lib, new):
     assert torch.isinf(o[new // 2:, :, 3]).all() and torch.isfinite(o[: new // 2]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,hq", [(1, 2), (6, 10), (50, 2)])
+def test_infinite_values_across_the_columns(gpu_lib, dtype, dim, new, hq):
+    """Infinite values and NaN in columns all over a row, in a tile that some rows see in part and in one that all do."""
+    b = Batch([700], [new], hq=hq, hkv=2, dim=dim, page=16, dtype=dtype, seed=dim + new)
+    for x in range(dim // 32):
+        b.put(0, 700 + new // 2, v=(INF, -INF)[x % 2], dims=32 * x + 5 * x % 32)
+    b.put(0, 320, v=INF, dims=dim - 1)
+    b.put(0, 700 + new - 1, v=NAN, dims=dim // 2)
+    b.put(0, 699, v=NAN, heads=1, dims=0)
+    o, lse = b.call(gpu_lib)
+    b.check(o, lse)
+    b.check(*b.call(gpu_lib, window=9), window=9)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (BF, 256), (F32, 64), (F32, 128), (F32, 256)])
+@pytest.mark.parametrize("new", [1, 7])
+def test_many_tiles_a_wave(gpu_lib, dtype, dim, new):
+    """Few rows over an axis so long that every wave of every workgroup goes through many tiles."""
+    b = Batch([16000, 40, 20011], [new, 0, new], hq=8, hkv=4, dim=dim, page=64, dtype=dtype, seed=dim + new)
+    b.check(*b.call(gpu_lib))
+    b.check(*b.call(gpu_lib, window=9001), window=9001)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_large_scores(gpu_lib, new):
     """Scores far apart: one key takes all the weight; the running maximum moves by hundreds."""
