@@ -613,16 +613,27 @@ def _paged_attn_bytes(*fields) -> int:
     return int(_lib.load().rglru_paged_attn_workspace_bytes(ctypes.byref(_paged_shape(*fields))))
 
 
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(device) -> int:
+    """The current stream's handle; without the Stream object that current_stream makes first (1.9 -> 0.1 us)."""
+    if _raw_stream_of is None or device.index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream_of(device.index)
+
+
 def _call_on(device, fn, where, *args):
     """Calls a library function on the current stream of `device` (made current for it where another one is)."""
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors are on {device}, expected a GPU")
     if device.index is None or device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+        status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _lib.check(status, where)
+            status = fn(*args, _raw_stream(device))
+    if status != 0:
+        _lib.check(status, where)
 
 
 def _int32(name, value, least=0):
