@@ -701,6 +701,10 @@ struct Wide {
   // bf16: two waves per SIMD, so that one's softmax runs beside the other's products. float32 products take 16 times as
   // long and hide the softmax by themselves: one wave per SIMD, half as many rows left idle
   static constexpr int kWaves = kBf16 ? 8 : 4;
+  // Workgroups on a CU: two where the registers allow it (float32, D = 64), so that one's softmax runs beside the other's
+  // products (2048 tokens after 8000, 4 key heads: 378 -> 337 us), but one for calls whose stretches would be shorter than
+  // kShort tiles (5 chunks of 111 to 294 tokens: 33 us with one, 37 with two; 10 of 200 after 500, 6 tiles: 53 and 50).
+  static constexpr int kGroups = !kBf16 && D == 64 ? 2 : 1, kShort = 4;
   static constexpr int kThreads = kWaves * 64;
   static constexpr int kRows = kWaves * 32;
   static constexpr int kKeys = D == 256 || !kBf16 ? 32 : 64;
@@ -772,6 +776,7 @@ __device__ __forceinline__ void list_row_tiles(const AttnArgs& a, int64_t* part,
 
 constexpr int kSchedThreads = 1024;
 constexpr int kOwnTiles = 256;
+constexpr int kCus = 256;   // of the card
 
 template <typename W>
 __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
@@ -1159,13 +1164,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
 constexpr int kSlackPart = 32;  // a cut moves by up to this part of a stretch (an eighth of it to a 64th measured the same)
 
 template <typename E, int D>
-__global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) void wide_kernel(AttnArgs a) {
+__global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4 * Wide<E, D>::kGroups)) void wide_kernel(AttnArgs a) {
   using P = Wide<E, D>;
   __shared__ __align__(1024) unsigned char buf[4 * P::kTileBytes];
   __shared__ int odd_waves[P::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
-  const int b = int(blockIdx.x % 8) * (a.wide.grid / 8) + int(blockIdx.x / 8);
   // The row tiles, from memory or listed here.
   __shared__ int64_t own_sched[2 + kOwnTiles], own_starts[kFewSeqs], scan_part[P::kWaves];
   __shared__ RowTile own_tiles[kOwnTiles];
@@ -1176,11 +1179,14 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4)) v
   const int64_t* const sched = a.own_list ? own_sched : a.sched;
   const int64_t count = uniform(sched[0]), per_head = uniform(sched[1]);
   const int64_t total = per_head * a.Hkv;
+  // Workgroups go to the 8 XCDs in turn: neighbouring stretches, which read the same keys, share an L2.
+  const int grid = P::kGroups > 1 && total < int64_t(P::kShort) * a.wide.grid ? min(a.wide.grid, kCus) : a.wide.grid;
+  const int b = int(blockIdx.x) < grid ? int(blockIdx.x % 8) * (grid / 8) + int(blockIdx.x / 8) : int(blockIdx.x);
   if (tid == 0) a.wide.joins[4 * b + 2] = 0;
   if (total == 0) return;
   // Short stretches, so that small calls spread: one sequence of 500 keys and 500 rows at D = 256 takes 30 us with 5 tiles
   // at least, 27 with 3, 28 with 1.
-  const Line line(total, a.wide.grid, 1 + P::kOver / 4);
+  const Line line(total, grid, 1 + P::kOver / 4);
   const int64_t* const before = sched + 2;
   // The unit that holds position `at`: key head, row tile, start.
   auto find = [&](int64_t at, int& head, int& tile, int64_t& start, int64_t& size) {
@@ -1430,7 +1436,7 @@ Plan plan_of(const rglru_paged_shape_t& s) {
   if (p.wide) {
     p.max_tiles = ceil_div(s.n_tokens * group, W::kRows) + seqs;
     p.own_list = !p.narrow && p.max_tiles <= kOwnTiles;
-    p.wide_grid = (grid_of(256, p.max_tiles * s.kv_heads, ceil_div(keys, W::kKeys)) + 7) / 8 * 8;
+    p.wide_grid = (grid_of(256 * W::kGroups, p.max_tiles * s.kv_heads, ceil_div(keys, W::kKeys)) + 7) / 8 * 8;
     p.row_tiles = take(size_t(p.max_tiles) * sizeof(RowTile));
     p.sched = take(size_t(2 + p.max_tiles + s.n_seqs) * 8);
     p.wide_joins = take(size_t(p.wide_grid) * 16);
