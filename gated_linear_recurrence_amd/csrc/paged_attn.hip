@@ -699,7 +699,7 @@ template <typename E, int D>
 struct Wide {
   static constexpr bool kBf16 = sizeof(E) == 2;
   // bf16: two waves per SIMD, so that one's softmax runs beside the other's products. float32 products take 16 times as
-  // long and hide the softmax by themselves: one wave per SIMD, half as many rows left idle
+  // long, so less shows of the softmax: one wave per SIMD in a workgroup, half as many rows left idle
   static constexpr int kWaves = kBf16 ? 8 : 4;
   // Workgroups on a CU: two where the registers allow it (float32, D = 64), so that one's softmax runs beside the other's
   // products (2048 tokens after 8000, 4 key heads: 378 -> 337 us), but one for calls whose stretches would be shorter than
