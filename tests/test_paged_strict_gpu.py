@@ -1,0 +1,54 @@
+"""Paged attention where answers are infinite, NaN or empty, held to the definition by the strict check."""
+import pytest
+import torch
+
+from _paged_strict import StrictBatch
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,hq", [(1, 2), (6, 10), (50, 2)])
+def test_infinities_keep_their_sign_and_place(gpu_lib, dtype, dim, new, hq):
+    """Infinite values and NaN in columns all over a row, in a tile that some rows see in part and in one that all do."""
+    b = StrictBatch([700], [new], hq=hq, hkv=2, dim=dim, page=16, dtype=dtype, seed=dim + new)
+    for x in range(dim // 32):
+        b.put(0, 700 + new // 2, v=(INF, -INF)[x % 2], dims=32 * x + 5 * x % 32)
+    b.put(0, 320, v=INF, dims=dim - 1)
+    b.put(0, 321, v=-INF, dims=dim - 2)
+    b.put(0, 700 + new - 1, v=NAN, dims=dim // 2)
+    b.put(0, 699, v=NAN, heads=1, dims=0)
+    b.put(0, 330, v=INF, dims=1)              # both signs: NaN
+    b.put(0, 700, v=-INF, dims=1)
+    b.check(*b.call(gpu_lib))
+    b.check(*b.call(gpu_lib, window=9), window=9)
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF, 64), (BF, 128), (BF, 256), (F32, 64), (F32, 256)])
+@pytest.mark.parametrize("new", [1, 5, 80])
+def test_rows_before_the_start(gpu_lib, dtype, dim, new):
+    """More new tokens than the cache holds: o = 0 and lse = -inf in every sequence's first rows. Lengths of zero."""
+    b = StrictBatch([0] * 4, [new] * 4, hq=4, hkv=2, dim=dim, page=16, dtype=dtype, kv_lens=[0, max(new - 1, 0), new, new + 3], pad=2,
+                    seed=new)
+    b.check(*b.call(gpu_lib))
+    b.check(*b.call(gpu_lib, window=2), window=2)
+
+
+def test_many_empty_rows_in_a_batch(gpu_lib):
+    b = StrictBatch([0] * 40, [3, 1, 0, 120] * 10, hq=4, hkv=1, dim=64, page=16, kv_lens=[i % 7 * (i % 4) for i in range(40)], pad=4, seed=6)
+    b.check(*b.call(gpu_lib))
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_infinite_columns_of_split_rows(gpu_lib, new):
+    """Infinite values in pieces of a row that the join merges."""
+    b = StrictBatch([9000, 3000], [new, new], hq=4, hkv=1, dim=128, page=64, seed=new)
+    for j, d in ((3, 0), (4000, 1), (8990, 2)):
+        b.put(0, j, v=INF, dims=d)
+        b.put(0, j + 1, v=-INF, dims=d + 8)
+        b.put(0, j, v=NAN, dims=d + 16)
+    b.put(1, 2999, v=-INF, dims=5)
+    b.check(*b.call(gpu_lib))
