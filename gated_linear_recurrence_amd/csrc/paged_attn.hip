@@ -26,8 +26,6 @@
 // full are therefore looked at first; where one is not finite, products of 0/1
 // operands mark the (row, column) pairs that see a +inf, a -inf or a NaN, and
 // those values are replaced by 0 in LDS before the tile is worked on.
-#include <cfloat>
-
 #include <hip/hip_runtime.h>
 
 #include "paged_common.h"
@@ -418,10 +416,15 @@ struct Wave {
     const bool grow = top * a.scale2 > c + kSlack;
     if (__any(grow)) {
       const float m_new = grow ? fmaxf(m, top) : m, c_new = m_new * a.scale2;
-      // never 0, so that an infinite output stays one (the smallest float leaves nothing else behind)
-      const float keep = grow && c != -INFINITY ? fmaxf(__builtin_amdgcn_exp2f(c - c_new), FLT_MIN) : 1.0f;
+      // 0 below 2^-126: a finite output leaves nothing then, an infinite one stays (this tile's marks may be among them).
+      // Rows that had no maximum have nothing to rescale, so a unit's first tile skips it (few rows at D = 256 17.4 -> 15.8 us).
+      const float keep = grow && c != -INFINITY ? __builtin_amdgcn_exp2f(c - c_new) : 1.0f;
+      if (__any(keep != 1.0f)) {
 #pragma unroll
-      for (int x = 0; x < D / 32; ++x) o[x] *= keep;
+        for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[x][r] = fabsf(o[x][r]) == INFINITY ? o[x][r] : o[x][r] * keep;
+      }
       l *= keep;
       m = m_new;
       c = grow ? c_new : c;
