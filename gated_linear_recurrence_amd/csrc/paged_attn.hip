@@ -569,7 +569,7 @@ __device__ __forceinline__ void store4(uint8_t* p, float a, float b, float c, fl
   }
 }
 
-// The D outputs of one row times `f`, 16 bytes per lane and instruction. The two half-waves hold 4 elements each of every
+// The D outputs of one row times `f` (0 for a row without weights, whatever its sums are), 16 bytes per lane and instruction. The two half-waves hold 4 elements each of every
 // 8: for bf16 they trade, so that one has the 8 of an even group and the other those of the next.
 template <typename E, int D>
 __device__ __forceinline__ void store_row(uint8_t* to, const f32x16* o, float f, int h) {
@@ -579,7 +579,7 @@ __device__ __forceinline__ void store_row(uint8_t* to, const f32x16* o, float f,
     for (int k = 0; k < 4; k += 2) {
       float e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) e[j] = o[y][4 * k + j] * f;
+      for (int j = 0; j < 8; ++j) e[j] = f == 0.0f ? 0.0f : o[y][4 * k + j] * f;
       if constexpr (sizeof(E) == 2) {
         const auto a = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(e[0], e[1]), f32x2_to_bf16x2(e[4], e[5]), false, false);
         const auto b = __builtin_amdgcn_permlane32_swap(f32x2_to_bf16x2(e[2], e[3]), f32x2_to_bf16x2(e[6], e[7]), false, false);

@@ -52,3 +52,26 @@ def test_infinite_columns_of_split_rows(gpu_lib, new):
         b.put(0, j, v=NAN, dims=d + 16)
     b.put(1, 2999, v=-INF, dims=5)
     b.check(*b.call(gpu_lib))
+
+
+KINDS = [(BF, 64), (BF, 128), (BF, 256), (F32, 64), (F32, 128), (F32, 256)]
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("ctx,new,n,heads", [(20, 1, 1, 1), (20, 60, 1, 1), (9000, 1, 1, 1), (9000, 60, 1, 1), (20, 1, 70, 4), (20, 60, 36, 8)])
+def test_no_weights_over_values_that_are_not_finite(gpu_lib, dtype, dim, ctx, new, n, heads):
+    """All scores -inf: o = 0 and lse = -inf whatever the values are, in cut units and (of many) in whole ones."""
+    b = StrictBatch([ctx] * n + [5], [new] * (n + 1), hq=heads, hkv=heads, dim=dim, page=64, dtype=dtype, seed=dim + new)
+    b.q.copy_(b.q.abs() + 0.1)
+    b.d_q.copy_(b.q)
+    for i in range(n):
+        b.d_k[b.d_table[i].long()] = -INF
+        b.k[i].fill_(-INF)
+        for j, d in ((3, 0), (ctx // 2, 1), (ctx - 1, 2)):
+            b.put(i, j, v=INF, dims=d)
+            b.put(i, j + 1, v=-INF, dims=d + 8)
+            b.put(i, j, v=NAN, dims=d + 16)
+    o, lse = b.call(gpu_lib)
+    b.check(o, lse)
+    assert (o[: n * new] == 0).all() and (lse[: n * new] == -INF).all()
+    b.check(*b.call(gpu_lib, window=7), window=7)
