@@ -18,36 +18,41 @@ def expected(q, k, v, kv_len, window, scale):
     m, hq, d = q.shape
     g = hq // k.shape[0]
     r = {x: np.zeros((m, hq, d)) for x in ("o", "weight", "faint")}
-    r.update(loose=np.zeros((m, hq, d), bool), lse=np.full((m, hq), -np.inf), size=np.zeros((m, hq)), seen=np.zeros(m, np.int64))
-    for i in range(m):
-        p = kv_len - m + i
-        lo = max(0, p - window + 1) if window else 0
-        if p < 0:
-            continue
-        r["seen"][i] = p + 1 - lo
-        for h in range(hq):
-            kk, vv = k[h // g, lo:p + 1], v[h // g, lo:p + 1]
+    r.update(loose=np.zeros((m, hq, d), bool), lse=np.full((m, hq), -np.inf), size=np.zeros((m, hq)))
+    p = kv_len - m + np.arange(m)[:, None]
+    j = np.arange(kv_len)
+    sees = (j <= p) & (j > p - window if window else True)
+    r["seen"] = sees.sum(1)
+    some = r["seen"] > 0
+    if not some.any():
+        return r
+    for h in range(hq):
+        kk, vv = k[h // g], v[h // g]
+        with np.errstate(invalid="ignore"):
+            s = np.where(sees, scale * (q[:, h] @ kk.T), -np.inf)
+            size = np.where(sees, abs(scale) * (np.abs(q[:, h]) @ np.abs(kk).T), 0.0).max(1)
+            top = s.max(1)
+            w = np.exp(s - np.where(top == -np.inf, 0.0, top)[:, None])
+            r["size"][:, h] = size
+        alive = some & (top != -np.inf)
+        bad = alive & (np.isnan(top) | (top == np.inf))
+        w = np.where((alive & ~bad)[:, None], w, 0.0)
+        total = np.where(alive & ~bad, w.sum(1), 1.0)
+        odd = ~np.isfinite(vv)
+        fin = np.where(odd, 0.0, vv)
+        part = w / total[:, None]
+        o, size = part @ fin, np.abs(fin)
+        r["weight"][:, h] = part @ size
+        r["faint"][:, h] = np.where(w < FAINT, part, 0.0) @ size
+        hit = np.flatnonzero(odd.any(1))
+        for n in hit:   # the few keys with such a value
+            see, at = (sees[:, n] & alive)[:, None], odd[n] & ~np.isnan(vv[n])
             with np.errstate(invalid="ignore"):
-                s = scale * (kk @ q[i, h])
-                r["size"][i, h] = abs(scale) * (np.abs(kk) @ np.abs(q[i, h])).max()
-            if (s == -np.inf).all():
-                continue
-            if np.isnan(s).any() or (s == np.inf).any():
-                r["o"][i, h] = r["lse"][i, h] = np.nan
-                continue
-            w = np.exp(s - s.max())
-            total = w.sum()
-            r["lse"][i, h] = s.max() + np.log(total)
-            fin = np.where(np.isfinite(vv), vv, 0.0)
-            o = (w / total) @ fin
-            r["weight"][i, h] = (w / total) @ np.abs(fin)
-            r["faint"][i, h] = (np.where(w < FAINT, w, 0.0) / total) @ np.abs(fin)
-            up, down, nan = vv == np.inf, vv == -np.inf, np.isnan(vv)
-            o[up.any(0)] = np.inf
-            o[down.any(0)] = -np.inf
-            o[nan.any(0) | (up.any(0) & down.any(0))] = np.nan
-            r["o"][i, h] = o
-            r["loose"][i, h] = ((up | down) & (w < FAINT)[:, None]).any(0)
+                o = np.where(see & odd[n], np.where(np.isfinite(o), 0.0, o) + vv[n], o)
+            r["loose"][:, h] |= see & at & (w[:, n] < FAINT)[:, None]
+        o[bad] = np.nan
+        r["o"][:, h] = o
+        r["lse"][:, h] = np.where(bad, np.nan, np.where(alive, np.where(alive, top, 0.0) + np.log(total), -np.inf))
     return r
 
 

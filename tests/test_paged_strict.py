@@ -41,7 +41,10 @@ def test_the_definition_agrees_with_the_oracle(window):
             o, lse, _, size, seen = oracle_paged.attention(q, k, v, b.kv[i], window, 0.125)
         r = expected(q, k, v, b.kv[i], window, 0.125)
         assert np.allclose(r["o"], o, rtol=0, atol=1e-13, equal_nan=True)
-        assert (r["lse"] == lse).all() and np.allclose(r["size"], size, rtol=1e-14) and (r["seen"] == seen).all()
+        # the sums of both go in orders of their own: 64 products of a score of 20 at most and 43 weights, 2^-53 each
+        assert (np.isinf(r["lse"]) == np.isinf(lse)).all() and size.max() < 20
+        assert np.allclose(r["lse"], lse, rtol=0, atol=(64 * 20 + 43) * 2.0 ** -53)
+        assert np.allclose(r["size"], size, rtol=64 * 2.0 ** -53) and (r["seen"] == seen).all()
 
 
 def test_it_passes_the_answers_and_rejects_others():
