@@ -1045,17 +1045,17 @@ __global__ __launch_bounds__((Narrow<E, D>::kThreads), (Narrow<E, D>::kGroups)) 
         for (int v = 0; v < P::kWaves; ++v) {
           const float f = __builtin_amdgcn_exp2f(merge_c[v][qq] - base);
           const float4 z = *reinterpret_cast<const float4*>(sums + (v * 32 + qq) * kRow + d);
-          if (merge_c[v][qq] != -INFINITY) {
-            acc.x += f * z.x;
-            acc.y += f * z.y;
-            acc.z += f * z.z;
-            acc.w += f * z.w;
-            l += f * merge_l[v][qq];
-          }
+          // a part without weights counts too, by a factor of 0: what it saw may not have been finite
+          acc.x += f * z.x;
+          acc.y += f * z.y;
+          acc.z += f * z.z;
+          acc.w += f * z.w;
+          l += f * merge_l[v][qq];
         }
         const int col = x0 * 32 + d;
         if (whole) {
           const float inv = top == -INFINITY ? 0.0f : 1.0f / l;
+          if (top == -INFINITY) acc = {0, 0, 0, 0};
           const int64_t r = out_row(a, s, hk, qq);
           store4<E>(a.o + (r * D + col) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
           if (a.lse != nullptr && col == 0) a.lse[r] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * kLn2;
@@ -1108,8 +1108,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
   // The sets share a row's pieces where there are many and that takes fewer reads in a row than a set per row.
   const bool share = pieces > kShare && (rows + shares - 1) / shares * kAhead < pieces;
   const int set = tid / kLanes, d = (tid % kLanes) * 4;
-  auto write = [&](int q, float c, float l, const float4& acc) {
+  auto write = [&](int q, float c, float l, float4 acc) {
     const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
+    if (c == -INFINITY) acc = {0, 0, 0, 0};
     const int64_t r = out_row(a, s, hk, r0 + q);
     store4<E>(a.o + (r * D + d) * sizeof(E), acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     if (a.lse != nullptr && d == 0) a.lse[r] = c == -INFINITY ? -INFINITY : (c + log2f(l)) * kLn2;
@@ -1121,8 +1122,9 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
     z = *reinterpret_cast<const float4*>(part + q * D + d);
   };
   auto merge = [](float& c, float& l, float4& acc, float pc, float pl, const float4& z) {
-    if (pc == -INFINITY) return;
-    const float top = fmaxf(c, pc), f0 = __builtin_amdgcn_exp2f(c - top), f1 = __builtin_amdgcn_exp2f(pc - top);
+    // a piece without weights counts too, by a factor of 0: what it saw may not have been finite
+    const float top = fmaxf(c, pc), base = top == -INFINITY ? 0.0f : top;
+    const float f0 = __builtin_amdgcn_exp2f(c - base), f1 = __builtin_amdgcn_exp2f(pc - base);
     acc.x = acc.x * f0 + z.x * f1;
     acc.y = acc.y * f0 + z.y * f1;
     acc.z = acc.z * f0 + z.z * f1;
@@ -1140,12 +1142,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
       float4 z[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int i = i0 + k * step;
-        fetch(min(i, pieces - 1), q, pc[k], pl[k], z[k]);
-        if (i >= pieces) pc[k] = -INFINITY;
+        fetch(min(i0 + k * step, pieces - 1), q, pc[k], pl[k], z[k]);
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) merge(c, l, acc, pc[k], pl[k], z[k]);
+      for (int k = 0; k < kAhead; ++k)
+        if (i0 + k * step < pieces) merge(c, l, acc, pc[k], pl[k], z[k]);
     }
     if (!share) {
       if (q0 + set < rows) write(q, c, l, acc);
@@ -1157,6 +1158,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
     if (set == 0) {
       c = -INFINITY, l = 0.0f;
       acc = {0, 0, 0, 0};
+#pragma unroll 1  // 94 registers instead of 130 at D = 64, so that more workgroups are there (drafts 67.5 -> 65 us)
       for (int v = 0; v < kSets; ++v) merge(c, l, acc, c_s[v], l_s[v], acc_s[v][tid]);
       write(q, c, l, acc);
     }

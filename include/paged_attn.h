@@ -116,13 +116,13 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  * with scores, softmax and sums in float32. A row that sees no key (p < 0, or
  * all its scores -inf) gets o = 0 and lse = -inf. What a row does not see has
  * no influence on it, infinities and NaN included (at given lengths not on a
- * bit of it); padding rows of o and lse are left as they were. Weights
- * of 2^-118 of a row's largest and less may count as nothing: a finite value adds
- * nothing there, an infinite one gives infinity or NaN. Sums are formed with
- * weights up to 2^8 and divided at the end, so of n visible values none should pass
- * 3.4e38 / (2^8 n), or they may overflow. For bf16 the softmax weights are rounded to bf16 where they enter the product
- * with the values (2^-8 relative at most). The same call gives the same bits
- * each time.
+ * bit of it); padding rows of o and lse are left as they were. Weights of 2^-118
+ * of a row's largest and less, the 0 of a score of -inf among them, may count as
+ * nothing: a finite value adds nothing there, an infinite one gives infinity or
+ * NaN. Sums are formed with weights up to 2^8 and divided at the end, so of n
+ * visible values none should pass 3.4e38 / (2^8 n), or they may overflow. For
+ * bf16 the softmax weights are rounded to bf16 where they enter the product with
+ * the values (2^-8 relative at most). The same call gives the same bits each time.
  *
  *   cu_seqlens       : [N + 1] int32 as above.       kv_lens : [N] int32, new tokens included.
  *   block_table      : [N, max_pages] int32; pages outside the cache give

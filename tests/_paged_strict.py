@@ -12,7 +12,7 @@ FAINT = 2.0 ** -117   # weights of 2^-118 of a row's largest may count as nothin
 def expected(q, k, v, kv_len, window, scale):
     """One sequence from the definition in float64: q [m, Hq, D], k and v [Hkv, kv_len, D].
 
-    Returns a dict of o and lse; weight, size and seen as oracle.paged.attention has them, over the finite values; faint:
+    Returns a dict of o and lse; weight, size and seen as oracle.paged.attention has them, over what is finite; faint:
     what weights below FAINT add at most; loose: where o is infinite by a weight below FAINT, so that NaN stands for it too.
     """
     m, hq, d = q.shape
@@ -30,10 +30,10 @@ def expected(q, k, v, kv_len, window, scale):
         kk, vv = k[h // g], v[h // g]
         with np.errstate(invalid="ignore"):
             s = np.where(sees, scale * (q[:, h] @ kk.T), -np.inf)
-            size = np.where(sees, abs(scale) * (np.abs(q[:, h]) @ np.abs(kk).T), 0.0).max(1)
+            size = abs(scale) * (np.abs(q[:, h]) @ np.abs(kk).T)
             top = s.max(1)
             w = np.exp(s - np.where(top == -np.inf, 0.0, top)[:, None])
-            r["size"][:, h] = size
+            r["size"][:, h] = np.where(sees & np.isfinite(size), size, 0.0).max(1)
         alive = some & (top != -np.inf)
         bad = alive & (np.isnan(top) | (top == np.inf))
         w = np.where((alive & ~bad)[:, None], w, 0.0)
@@ -74,7 +74,7 @@ class StrictBatch(Batch):
             k, v = (t[i].double().numpy().transpose(1, 0, 2) for t in (self.k, self.v))
             r = expected(self.q[rows].double().numpy(), k, v, self.kv[i], window, scale)
             ref, ref_lse = r["o"], r["lse"]
-            e = (self.dim + 8) * 2.0 ** -24 * np.where(np.isfinite(r["size"]), r["size"], 0.0)
+            e = (self.dim + 8) * 2.0 ** -24 * r["size"]
             sums = ((r["seen"] + 8) * 2.0 ** -23)[:, None]
             fin, lfin = np.isfinite(ref), np.isfinite(ref_lse)
             size = np.where(fin, np.abs(ref), 0.0)

@@ -75,3 +75,23 @@ def test_no_weights_over_values_that_are_not_finite(gpu_lib, dtype, dim, ctx, ne
     b.check(o, lse)
     assert (o[: n * new] == 0).all() and (lse[: n * new] == -INF).all()
     b.check(*b.call(gpu_lib, window=7), window=7)
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("new", [1, 3, 60])
+@pytest.mark.parametrize("ctx,n", [(250, 70), (9000, 2)])
+def test_values_that_are_not_finite_at_scores_of_minus_infinity(gpu_lib, dtype, dim, new, ctx, n):
+    """The first half of the keys scores -inf and has infinite values: their weight of 0 gives infinity or NaN, never a number,
+    whichever wave or piece of the row they fell to."""
+    b = StrictBatch([ctx] * n, [new] * n, hq=2, hkv=2, dim=dim, page=64, dtype=dtype, seed=dim + new)
+    b.q.copy_(b.q.abs() + 0.1)
+    b.d_q.copy_(b.q)
+    pages = ctx // 2 // 64
+    for i in range(n):
+        b.d_k[b.d_table[i, :pages].long()] = -INF
+        b.k[i][: pages * 64].fill_(-INF)
+        for j, d in ((3, 0), (40, 1), (pages * 64 - 1, 2)):
+            b.put(i, j, v=INF, dims=d)
+            b.put(i, j, v=-INF, dims=d + 8)
+            b.put(i, j, v=NAN, dims=d + 16)
+    b.check(*b.call(gpu_lib))
