@@ -712,7 +712,8 @@ def rglru_page_plan(context_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_
     entries) are updated in place: pages past a sequence's new length go back to the stack, then new ones are
     popped in the order of sequences. max_new: the most new tokens of a sequence, 0 if not known.
     Returns (slot_map [T], positions [T], kv_lens [N], held_lens_out [N], free_count_out [1], unserved [1]); a
-    sequence for which no pages are left is counted in unserved, its slots are -1, its lengths and pages stay."""
+    sequence for which no pages are left is counted in unserved, its slots are -1, its lengths and pages stay; attention
+    on these lengths gives its rows unspecified values, to be dropped where slot_map is -1."""
     lib = _lib.load()
     dev = context_lens.device
     n = _packed(cu_seqlens, dev)

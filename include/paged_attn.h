@@ -67,7 +67,10 @@ typedef struct {
  *     the same order (the page given back last goes first). A sequence is
  *     served if its row has need_n columns and the list still holds its pages
  *     after all sequences before it asked for theirs; one that is not served
- *     takes none and its row is left as it was.
+ *     takes none and its row is left as it was. cu_seqlens still counts its
+ *     tokens: they have slot -1, the write skips them, and rglru_paged_attn_fwd on
+ *     this step's lengths gives their rows unspecified values (it takes them to
+ *     stand at the context's end), which the caller drops wherever slot_map is -1.
  *
  *   context_lens : [N] int32, tokens in the cache before the step, at most held_lens.
  *   held_lens    : [N] int32, tokens the row's pages were taken for (the last
