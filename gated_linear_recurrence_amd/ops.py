@@ -778,7 +778,8 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     last `window` of them. max_new: the most new tokens of a sequence (0: not known; 1 for a decode step picks the
     kernel for few rows). scale defaults to 1 / sqrt(D). workspace: a uint8 device tensor of at least
     rglru_paged_attn_workspace_bytes bytes, 256-byte aligned (allocated here when None; a captured step of many
-    layers should pass one, it is up to 140 MB); calls sharing one must not overlap. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
+    layers should pass one: it is up to 153 MB, and more for very many rows); calls sharing one must not overlap.
+    Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
     lib = _lib.load()
     dev = k_cache.device
     n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)

@@ -134,9 +134,12 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *   k_cache, v_cache : [n_pages, Hkv, page_size, D] io, 16-byte aligned.
  *   o                : [T, Hq, D] io, dense, 16-byte aligned.
  *   lse              : NULL or [T, Hq] float32.
- *   workspace        : rglru_paged_attn_workspace_bytes(shape) bytes (up to some
- *                      140 MB, whatever the lengths), 256-byte aligned; calls
- *                      that share one must not overlap in time. */
+ *   workspace        : rglru_paged_attn_workspace_bytes(shape) bytes, 256-byte
+ *                      aligned: up to 153 MB (D = 256 in bf16, prompt chunks among
+ *                      more than 16 sequences) whatever the lengths, 40 bytes for
+ *                      every 128 rows of n_tokens * q_heads / kv_heads (256 in
+ *                      bf16) and 48 for every sequence. Calls that share one must
+ *                      not overlap in time. */
 size_t rglru_paged_attn_workspace_bytes(const rglru_paged_shape_t* shape);
 rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* shape, const int32_t* cu_seqlens,
                                     const int32_t* kv_lens, const int32_t* block_table, const void* q,

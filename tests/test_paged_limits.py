@@ -1,0 +1,32 @@
+"""Limits of the paged-cache entry points, without a GPU: sizes as documented, and refusals that come before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import gated_linear_recurrence_amd as glr
+from gated_linear_recurrence_amd import _lib
+
+
+def shape(**kw):
+    fields = dict(n_tokens=40, n_pages=100, n_seqs=3, max_pages=30, page_size=16, q_heads=8, kv_heads=2, head_dim=128,
+                  io_dtype=_lib.RGLRU_IO_BF16, scale=0.1)
+    return _lib.rglru_paged_shape_t(**{**fields, **kw})
+
+
+def test_workspace_bytes_are_within_what_the_header_says():
+    """153 MB, 40 bytes for every row tile (128 rows of float32, 256 of bf16) and 48 for every sequence; 153 MB is not too much by
+    more than a hundredth."""
+    most = 0
+    for io, rows in ((_lib.RGLRU_IO_BF16, 256), (_lib.RGLRU_IO_F32, 128)):
+        for dim in (64, 128, 256):
+            for n in (1, 16, 17, 1000, 1 << 16):
+                for t in (1, 300, 20000, 1 << 22, (1 << 27) - (1 << 13)):
+                    for hq, hkv in ((1, 1), (16, 1), (16, 16)):
+                        for new in (0, 1):
+                            need = glr.rglru_paged_attn_workspace_bytes(shape(
+                                n_tokens=t, n_seqs=n, q_heads=hq, kv_heads=hkv, head_dim=dim, io_dtype=io, max_new=new, max_pages=8000))
+                            extra = 40 * -(-t * (hq // hkv) // rows) + 48 * n
+                            assert 0 < need <= 153e6 + extra, (io, dim, n, t, hq, hkv, new)
+                            most = max(most, need - extra)
+    assert most > 0.99 * 153e6
