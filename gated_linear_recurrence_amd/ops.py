@@ -698,6 +698,17 @@ def _out(t, name, shape, dtype, device):
     return torch.empty(shape, dtype=dtype, device=device) if t is None else _need(t, name, shape, dtype, device)
 
 
+def _scratch(t, device):
+    """Checks a workspace of any contents: not a Workspace's, whose contents the recurrent calls count on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a uint8 tensor of its own (a Workspace's contents must stay)")
+    if t.device != device or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    at = t.untyped_storage().data_ptr()
+    if any(w.buf is not None and w.buf.untyped_storage().data_ptr() == at for w in list(_workspaces)):
+        raise ValueError("workspace is a Workspace's buffer, whose contents must stay")
+
+
 def rglru_page_plan(context_lens: torch.Tensor, cu_seqlens: torch.Tensor, block_table: torch.Tensor,
                     free_pages: torch.Tensor, free_count: torch.Tensor, *, n_tokens: int, page_size: int,
                     held_lens: Optional[torch.Tensor] = None, max_new: int = 0,
@@ -778,8 +789,8 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     last `window` of them. max_new: the most new tokens of a sequence (0: not known; 1 for a decode step picks the
     kernel for few rows). scale defaults to 1 / sqrt(D). workspace: a uint8 device tensor of at least
     rglru_paged_attn_workspace_bytes bytes, 256-byte aligned (allocated here when None; a captured step of many
-    layers should pass one: it is up to 153 MB, and more for very many rows); calls sharing one must not overlap.
-    Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
+    layers should pass one: it is up to 153 MB, and more for very many rows), of any contents and not a Workspace's,
+    whose contents must stay; calls sharing one must not overlap. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding rows are left as they were."""
     lib = _lib.load()
     dev = k_cache.device
     n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)
@@ -798,8 +809,8 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
               _int32("window", window), sc, row, 0)
     if workspace is None:
         workspace = torch.empty(max(_paged_attn_bytes(*fields), 1), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    else:
+        _scratch(workspace, dev)
     _call_on(dev, lib.rglru_paged_attn_fwd, "rglru_paged_attn_fwd", ctypes.byref(_paged_shape(*fields)),
              cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel())

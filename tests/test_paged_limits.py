@@ -30,3 +30,22 @@ def test_workspace_bytes_are_within_what_the_header_says():
                             assert 0 < need <= 153e6 + extra, (io, dim, n, t, hq, hkv, new)
                             most = max(most, need - extra)
     assert most > 0.99 * 153e6
+
+
+def cpu_call(**kw):
+    kc, vc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16), torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    i = lambda *a: torch.tensor(a, dtype=torch.int32)  # noqa: E731
+    return glr.rglru_paged_attn_fwd(torch.zeros(3, 4, 64, dtype=torch.bfloat16), kc, vc, i(0, 1).view(1, 2), i(0, 3), i(3), **kw)
+
+
+def test_a_recurrent_workspace_is_not_taken():
+    """The recurrent calls count on what their Workspace holds, so neither it nor its buffer serves as scratch memory here."""
+    ws = glr.Workspace("cpu")
+    with pytest.raises(TypeError, match="Workspace"):
+        cpu_call(workspace=ws)
+    buf = ws.get(1 << 20)
+    for part in (buf, buf[4096:]):
+        with pytest.raises(ValueError, match="Workspace"):
+            cpu_call(workspace=part)
+    with pytest.raises(ValueError, match="expected a GPU"):   # a buffer of its own passes that check
+        cpu_call(workspace=torch.zeros(1 << 20, dtype=torch.uint8))
