@@ -1386,10 +1386,14 @@ __global__ __launch_bounds__((Wide<E, D>::kThreads), (Wide<E, D>::kWaves / 4 * W
   }
 }
 
+// |scale| log2 e, which multiplies the scores.
+float log2_scale(float scale) { return std::fabs(scale) * kLog2e; }
+
 rglru_status_t check(const rglru_paged_shape_t& s) {
   if (!valid_pages(s) || !valid_table(s) || !valid_io(s) || s.kv_heads < 1 || s.q_heads < s.kv_heads ||
       s.q_heads > (1 << 14) || s.q_heads % s.kv_heads != 0 || s.n_tokens * s.q_heads > (int64_t(1) << 31) - (1 << 16) ||
-      s.head_dim < 1 || s.head_dim > (1 << 16) || s.window < 0 || !std::isfinite(s.scale) ||
+      s.head_dim < 1 || s.head_dim > (1 << 16) || s.window < 0 ||
+      !std::isfinite(log2_scale(s.scale)) ||
       row_stride(s.q_stride, int64_t(s.q_heads) * s.head_dim) < 0)
     return RGLRU_ERR_INVALID_ARGUMENT;
   if (s.head_dim != 64 && s.head_dim != 128 && s.head_dim != 256) return RGLRU_ERR_UNSUPPORTED;
@@ -1546,7 +1550,7 @@ extern "C" rglru_status_t rglru_paged_attn_fwd(const rglru_paged_shape_t* sp, co
   a.Hkv = s.kv_heads;
   a.group = s.q_heads / s.kv_heads;
   a.window = s.window < int64_t(s.max_pages) * s.page_size ? s.window : 0;  // a window as long as the row hides nothing
-  a.scale2 = s.scale == 0.0f ? 1.0f : std::fabs(s.scale) * paged::kLog2e;
+  a.scale2 = s.scale == 0.0f ? 1.0f : paged::log2_scale(s.scale);
   a.q_sign = s.scale > 0.0f ? 1 : s.scale < 0.0f ? -1 : 0;
   RGLRU_PAGED_DISPATCH(s, paged::launch, s, a, static_cast<uint8_t*>(workspace), static_cast<hipStream_t>(stream));
   return launch_status();

@@ -32,8 +32,8 @@ extern "C" {
  * 2^16; page_size a power of two from 8 to 1024; n_pages >= 1 with n_pages *
  * page_size < 2^31; max_pages >= 1 with max_pages * page_size <= 2^31 - 2^16; 1 <= kv_heads <= q_heads <= 2^14 with
  * q_heads a multiple of kv_heads; n_tokens * q_heads <= 2^31 - 2^16; head_dim >= 1;
- * io_dtype an rglru_io_t; max_new, window >= 0; a finite scale; strides 0 or
- * at least the dense row. Within them, a head_dim other than 64, 128 or 256
+ * io_dtype an rglru_io_t; max_new, window >= 0; |scale| <= 2.35e38 (times log2 e it
+ * has to be finite); strides 0 or at least the dense row. Within them, a head_dim other than 64, 128 or 256
  * is RGLRU_ERR_UNSUPPORTED, and a stride that is not a multiple of 16 bytes
  * RGLRU_ERR_MISALIGNED. An output (what is updated in place and the workspace
  * too) that overlaps another one or an input is RGLRU_ERR_INVALID_ARGUMENT;
@@ -116,7 +116,7 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *
  *   o   = sum_j softmax_j(scale q . k_j) v_j        lse = ln sum_j exp(scale q . k_j)
  *
- * with scores, softmax and sums in float32. A row that sees no key (p < 0, or
+ * with q . k, scores, softmax and sums in float32, the scale applied to q . k. A row that sees no key (p < 0, or
  * all its scores -inf) gets o = 0 and lse = -inf. What a row does not see has
  * no influence on it, infinities and NaN included (at given lengths not on a
  * bit of it); padding rows of o and lse are left as they were. Weights of 2^-118

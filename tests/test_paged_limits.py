@@ -49,3 +49,18 @@ def test_a_recurrent_workspace_is_not_taken():
             cpu_call(workspace=part)
     with pytest.raises(ValueError, match="expected a GPU"):   # a buffer of its own passes that check
         cpu_call(workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def raw_attn(s):
+    """The library's answer to a call with no workspace, which is refused at the latest for that."""
+    at = ctypes.c_void_p(0x100000)
+    return _lib.load().rglru_paged_attn_fwd(ctypes.byref(s), *[at] * 9, 0, None)
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scales_past_float32_in_log2_units(sign):
+    """scale log2 e has to be a float32: 3.4e38 / 1.4427 = 2.3586e38 is the largest."""
+    for scale, status in ((2.35e38, 3), (2.37e38, 1), (3.4e38, 1)):
+        s = shape(scale=sign * scale)
+        assert raw_attn(s) == status
+        assert (glr.rglru_paged_attn_workspace_bytes(s) > 0) == (status == 3)
