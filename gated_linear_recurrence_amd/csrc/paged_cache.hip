@@ -311,7 +311,7 @@ extern "C" rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* sp, co
   if (s.head_dim * esize % 16 != 0) return RGLRU_ERR_UNSUPPORTED;
   const int64_t per_token = dense * esize / 16;
   const int64_t pieces = s.n_tokens * per_token;
-  if (ceil_div(pieces, paged::kWriteThreads) >= (int64_t(1) << 31)) return RGLRU_ERR_INVALID_ARGUMENT;
+  if (ceil_div(pieces, paged::kWriteThreads) * paged::kWriteThreads >= (int64_t(1) << 32)) return RGLRU_ERR_INVALID_ARGUMENT;
   if (s.n_tokens > 0 && (k == nullptr || v == nullptr || k_cache == nullptr || v_cache == nullptr || slot_map == nullptr))
     return RGLRU_ERR_INVALID_ARGUMENT;
   if (!aligned_to(k, 16) || !aligned_to(v, 16) || !aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) ||

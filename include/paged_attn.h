@@ -104,8 +104,9 @@ rglru_status_t rglru_page_plan(const rglru_paged_shape_t* shape, const int32_t* 
  *   k, v             : [T, Hkv, D] io, rows kv_stride apart, 16-byte aligned.
  *   k_cache, v_cache : [n_pages, Hkv, page_size, D] io, 16-byte aligned.
  *   slot_map         : [T] int32.
- * Reads the shape's n_tokens, n_pages, page_size, kv_heads, head_dim (any
- * multiple of 16 bytes here), io_dtype and kv_stride. */
+ * At most 2^36 - 2^12 bytes of keys a call. Reads the shape's n_tokens, n_pages,
+ * page_size, kv_heads, head_dim (any multiple of 16 bytes here), io_dtype and
+ * kv_stride. */
 rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void* k, const void* v, void* k_cache,
                                     void* v_cache, const int32_t* slot_map, void* stream);
 

@@ -64,3 +64,14 @@ def test_scales_past_float32_in_log2_units(sign):
         s = shape(scale=sign * scale)
         assert raw_attn(s) == status
         assert (glr.rglru_paged_attn_workspace_bytes(s) > 0) == (status == 3)
+
+
+@pytest.mark.parametrize("tokens,heads,dim,io,status", [
+    (1 << 24, 128, 16, _lib.RGLRU_IO_BF16, 1), ((1 << 24) - 1, 128, 16, _lib.RGLRU_IO_BF16, 2),
+    ((1 << 31) - 1, 2, 4, _lib.RGLRU_IO_F32, 1), ((1 << 31) - 128, 2, 4, _lib.RGLRU_IO_F32, 2), ((1 << 31) - 1, 1 << 14, 64, _lib.RGLRU_IO_F32, 1)])
+def test_writes_of_more_threads_than_a_launch_has(tokens, heads, dim, io, status):
+    """A thread moves 16 bytes of keys and of values, and a launch has less than 2^32 threads, in blocks of 256: 2^36 - 2^12 bytes of
+    keys. A smaller call passes that check (and is refused for its alignment here)."""
+    s = shape(n_tokens=tokens, kv_heads=heads, head_dim=dim, io_dtype=io)
+    odd = ctypes.c_void_p(0x100008)
+    assert _lib.load().rglru_paged_kv_write(ctypes.byref(s), *[odd] * 5, None) == status
