@@ -655,7 +655,10 @@ def _paged_cache(k_cache, v_cache, device):
         raise ValueError(f"unsupported dtype {k_cache.dtype}")
     _need(k_cache, "k_cache", k_cache.shape, k_cache.dtype, device)
     _need(v_cache, "v_cache", k_cache.shape, k_cache.dtype, device)
-    return k_cache.shape
+    shape = k_cache.shape
+    if max(shape[1], shape[2], shape[3]) >> 31:
+        raise ValueError(f"k_cache has shape {tuple(shape)}, expected heads, page size and width below 2^31")
+    return shape
 
 
 def _rows(t, name, heads, dim, dtype, device):
@@ -682,7 +685,7 @@ def _rows(t, name, heads, dim, dtype, device):
 def _packed(cu_seqlens, device):
     if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [N + 1]")
-    n = cu_seqlens.numel() - 1
+    n = _int32("the number of sequences", cu_seqlens.numel() - 1)
     _need(cu_seqlens, "cu_seqlens", (n + 1,), torch.int32, device)
     return n
 
@@ -691,7 +694,7 @@ def _table(block_table, n, device):
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [N, max_pages]")
     _need(block_table, "block_table", (n, block_table.shape[1]), torch.int32, device)
-    return block_table.shape[1]
+    return _int32("max_pages", block_table.shape[1])
 
 
 def _out(t, name, shape, dtype, device):
@@ -796,7 +799,7 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     n_pages, heads, page_size, dim = _paged_cache(k_cache, v_cache, dev)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [T, Hq, D]")
-    hq = q.shape[1]
+    hq = _int32("Hq", q.shape[1])
     t, row = _rows(q, "q", hq, dim, k_cache.dtype, dev)
     n = _packed(cu_seqlens, dev)
     _need(kv_lens, "kv_lens", (n,), torch.int32, dev)

@@ -75,3 +75,33 @@ def test_writes_of_more_threads_than_a_launch_has(tokens, heads, dim, io, status
     s = shape(n_tokens=tokens, kv_heads=heads, head_dim=dim, io_dtype=io)
     odd = ctypes.c_void_p(0x100008)
     assert _lib.load().rglru_paged_kv_write(ctypes.byref(s), *[odd] * 5, None) == status
+
+
+def test_sizes_that_do_not_fit_32_bits():
+    """Sizes that come from a tensor's shape are checked like those that are passed (they would wrap in the shape's 32-bit fields).
+    Tensors without memory stand for the large ones."""
+    m = lambda *a, dtype=torch.int32: torch.empty(a, dtype=dtype, device="meta")  # noqa: E731
+    big, bf = (1 << 32) + 1, torch.bfloat16
+    cache = m(4, 2, 16, 64, dtype=bf)
+    attn = [m(3, 4, 64, dtype=bf), cache, cache, m(1, 2), m(2), m(1)]
+
+    def with_(at, *values):
+        out = list(attn)
+        out[at:at + len(values)] = values
+        return out
+
+    for args in (with_(0, m(3, big * 2, 64, dtype=bf)), with_(1, *[m(4, 2, (1 << 32) + 16, 64, dtype=bf)] * 2),
+                 with_(0, m(3, 4, (1 << 32) + 64, dtype=bf), *[m(4, 2, 16, (1 << 32) + 64, dtype=bf)] * 2),
+                 with_(1, *[m(4, (1 << 32) + 2, 16, 64, dtype=bf)] * 2), with_(3, m(1, big)), with_(3, m(big, 2), m(big + 1), m(big))):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            glr.rglru_paged_attn_fwd(*args)
+    k = m(3, 2, 64, dtype=bf)
+    for kk, c in ((k, m(4, 2, (1 << 32) + 16, 64, dtype=bf)), (m(3, big, 64, dtype=bf), m(4, big, 16, 64, dtype=bf)),
+                  (m(3, 2, (1 << 32) + 64, dtype=bf), m(4, 2, 16, (1 << 32) + 64, dtype=bf))):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            glr.rglru_paged_kv_write(kk, kk, c, c, m(3))
+    for n, width in ((1, big), (big, 1)):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            glr.rglru_page_plan(m(n), m(n + 1), m(n, width), m(8), m(1), n_tokens=1, page_size=16)
+    with pytest.raises(ValueError, match="expected a GPU"):
+        glr.rglru_paged_attn_fwd(*attn)
