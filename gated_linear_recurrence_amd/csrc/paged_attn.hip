@@ -313,7 +313,12 @@ struct Wave {
 #pragma unroll
     for (int x = 0; x < D / 16; ++x) {
       q[x].w = 0;
-      if (live) q[x] = *reinterpret_cast<const Frag<E>*>(src + (x * 16 + h * 8) * sizeof(E));
+      if (live) {
+        // in pieces of 16 bytes, which is what the rows are aligned to
+        const u32x4* const from = reinterpret_cast<const u32x4*>(src + (x * 16 + h * 8) * sizeof(E));
+        if constexpr (sizeof(E) == 2) q[x].w = from[0];
+        else q[x].w = __builtin_shufflevector(from[0], from[1], 0, 1, 2, 3, 4, 5, 6, 7);
+      }
     }
   }
 

@@ -95,3 +95,20 @@ def test_values_that_are_not_finite_at_scores_of_minus_infinity(gpu_lib, dtype, 
             b.put(i, j, v=-INF, dims=d + 8)
             b.put(i, j, v=NAN, dims=d + 16)
     b.check(*b.call(gpu_lib))
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("new", [1, 7, 70])
+def test_rows_aligned_to_16_bytes_and_no_more(gpu_lib, dtype, dim, new):
+    """Queries that start 16 bytes into wider rows of an odd number of 16-byte pieces, the outputs and the log-sum-exps of a like kind."""
+    b = StrictBatch([90, 300], [new, new], hq=6, hkv=2, dim=dim, page=16, dtype=dtype, pad=2, seed=new)
+    one = 16 // b.d_q.element_size()
+    rows = b.q.shape[0]
+    wide = torch.full((rows, 6 * dim + 3 * one), NAN, dtype=dtype, device="cuda")
+    q = wide[:, one:one + 6 * dim].unflatten(1, (6, dim))
+    q.copy_(b.q)
+    o = torch.full((rows * 6 * dim + one,), 7.0, dtype=dtype, device="cuda")[one:].view(rows, 6, dim)
+    lse = torch.full((rows * 6 + 1,), 7.0, device="cuda")[1:].view(rows, 6)
+    assert q.data_ptr() % 32 == o.data_ptr() % 32 == 16 and q.stride(0) * q.element_size() % 32 == 16
+    gpu_lib.rglru_paged_attn_fwd(q, b.d_k, b.d_v, b.d_table, b.d_cu, b.d_kv, o=o, lse=lse)
+    b.check(o, lse)
