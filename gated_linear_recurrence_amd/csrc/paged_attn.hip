@@ -646,9 +646,16 @@ struct Line {
 // ms, 5.5 TB/s; of 32 768 keys: 6.1 TB/s.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
 
-// With up to this many sequences in a call that needs the wide kernel, the wide kernel takes those of few rows too: a chunk of
-// 1000 tokens beside 11 single tokens over 2000 keys each takes 60 us so and 63 with both kernels, beside 23 75 and 70.
+// In a call that needs the wide kernel it takes the sequences of few rows too where there are at most kFewSeqs sequences and
+// kFewUnits (sequence of few rows, key head) pairs: it saves a launch, but works through such a unit as slowly as through
+// one of many rows. 618 calls of a chunk of 200 or 1000 tokens and 1 to 15 single tokens, all after 200 to 8000 tokens, 1
+// to 16 key heads, timed with the wide kernel alone and with both: taking the better of the two by this rule costs 1.6 %
+// more than by the clock in bf16 at D = 64 and 2.2 to 2.8 % in float32 (without the second bound 5 and 7 to 13 %), 0.2 %
+// in bf16 at D = 128 and 256, whose best bound is past what was measured (240). A chunk of 1000 after 2000 at D = 128, 4
+// key heads, alone and both: beside 15 single tokens 56 and 60 us, in float32 273 and 239; beside 47 87 and 78.
 constexpr int kFewSeqs = 16;
+template <typename E, int D>
+constexpr int kFewUnits = sizeof(E) == 4 ? 24 : D == 64 ? 64 : 256;
 
 template <typename E, int D>
 struct Narrow {
@@ -711,13 +718,15 @@ struct Wide {
   static constexpr int kWaves = kBf16 ? 8 : 4;
   // Workgroups on a CU: two where the registers allow it (float32, D = 64), so that one's softmax runs beside the other's
   // products (2048 tokens after 8000, 4 key heads: 378 -> 337 us), but one for calls whose stretches would be shorter than
-  // kShort tiles (5 chunks of 111 to 294 tokens: 33 us with one, 37 with two; 10 of 200 after 500, 6 tiles: 53 and 50).
-  static constexpr int kGroups = !kBf16 && D == 64 ? 2 : 1, kShort = 4;
+  // kShort tiles. 208 calls of 1 to 20 chunks of 50 to 1000 tokens after 0 to 2000, 2 to 8 key heads, timed with one and with two:
+  // one is up to 1.3 times as fast at 1 to 3 tiles, the same at 8 to 12, two 1.1 times as fast from 20 on.
+  static constexpr int kGroups = !kBf16 && D == 64 ? 2 : 1, kShort = 10;
   static constexpr int kThreads = kWaves * 64;
   static constexpr int kRows = kWaves * 32;
   static constexpr int kKeys = D == 256 || !kBf16 ? 32 : 64;
   // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
-  // (D = 128); float32 tiles take 16 times as long.
+  // (D = 128); float32 tiles take 16 times as long. At D = 64 126 calls (1 to 20 chunks of 100 to 2000 tokens after 0 to 4000,
+  // with and without a window) take 0.6 % more in the mean with 3 and 0.7 % more with 8.
   static constexpr int kOver = !kBf16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
   static constexpr int kTileBytes = kKeys * D * int(sizeof(E));
   static constexpr int kLoads = kTileBytes / 1024 / kWaves;  // per wave, keys and values each
@@ -1405,16 +1414,24 @@ rglru_status_t check(const rglru_paged_shape_t& s) {
   return RGLRU_OK;
 }
 
-// The largest number of rows of one sequence that the caller allows.
-int64_t most_rows(const rglru_paged_shape_t& s) {
-  const int64_t longest = s.max_new > 0 && s.max_new < s.n_tokens ? s.max_new : s.n_tokens;
-  return longest * (s.q_heads / s.kv_heads);
+// The largest number of tokens and of rows of one sequence that the caller allows.
+int64_t most_tokens(const rglru_paged_shape_t& s) { return s.max_new > 0 && s.max_new < s.n_tokens ? s.max_new : s.n_tokens; }
+int64_t most_rows(const rglru_paged_shape_t& s) { return most_tokens(s) * (s.q_heads / s.kv_heads); }
+
+// The largest number of sequences of few rows in a batch of n_tokens where the others have most_tokens at most, and those
+// have more than kNarrowRows rows.
+int64_t most_few(const rglru_paged_shape_t& s) {
+  const int64_t longest = most_tokens(s), few = kNarrowRows / (s.q_heads / s.kv_heads);
+  const int64_t x = (s.n_seqs * longest - s.n_tokens) / (longest - few);
+  return x < 0 ? 0 : x < s.n_seqs ? x : s.n_seqs;
 }
 
 // A call whose sequences may all have at most kNarrowRows rows runs the narrow
 // kernel alone (32 sequences of 4096 keys, 32 rows on each of 4 key heads of
 // 128: 60 us, the wide kernel 65); any other one the wide kernel, and before it
-// the narrow kernel for the sequences of few rows among more than kFewSeqs.
+// the narrow kernel for the sequences of few rows unless those are few themselves
+// (kFewSeqs, kFewUnits). The workspace has room for the narrow kernel wherever a
+// call of fewer tokens would run it, so one of the largest size serves all.
 struct Plan {
   bool narrow, wide, own_list;
   int narrow_grid, wide_grid;  // workgroups; of the wide kernel a multiple of 8
@@ -1427,7 +1444,8 @@ Plan plan_of(const rglru_paged_shape_t& s) {
   using W = Wide<E, D>;
   Plan p = {};
   p.wide = most_rows(s) > kNarrowRows;
-  p.narrow = !p.wide || s.n_seqs > kFewSeqs;
+  const bool room = !p.wide || s.n_seqs > kFewSeqs || int64_t(s.n_seqs) * s.kv_heads > kFewUnits<E, D>;
+  p.narrow = !p.wide || s.n_seqs > kFewSeqs || most_few(s) * s.kv_heads > kFewUnits<E, D>;
   const int64_t group = s.q_heads / s.kv_heads;
   const int64_t keys = int64_t(s.max_pages) * s.page_size;
   const int64_t seqs = s.n_seqs < s.n_tokens ? s.n_seqs : s.n_tokens;
@@ -1441,7 +1459,7 @@ Plan plan_of(const rglru_paged_shape_t& s) {
   auto grid_of = [](int64_t most, int64_t units, int64_t tiles) {
     return int(units >= most || tiles >= most || units * tiles >= most ? most : units * tiles > 0 ? units * tiles : 1);
   };
-  if (p.narrow) {
+  if (room) {
     using P = Narrow<E, D>;
     p.narrow_grid = grid_of(256 * P::kGroups, seqs * s.kv_heads, ceil_div(ceil_div(keys, kNarrowKeys), P::kWaves));
     p.narrow_joins = take(size_t(p.narrow_grid) * 16);
@@ -1456,6 +1474,7 @@ Plan plan_of(const rglru_paged_shape_t& s) {
     p.wide_joins = take(size_t(p.wide_grid) * 16);
     p.wide_parts = take(size_t(p.wide_grid) * 2 * part_floats<D>(W::kRows) * 4);
   }
+  if (!p.narrow) p.narrow_grid = 0;
   p.bytes = at;
   return p;
 }

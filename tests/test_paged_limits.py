@@ -105,3 +105,18 @@ def test_sizes_that_do_not_fit_32_bits():
             glr.rglru_page_plan(m(n), m(n + 1), m(n, width), m(8), m(1), n_tokens=1, page_size=16)
     with pytest.raises(ValueError, match="expected a GPU"):
         glr.rglru_paged_attn_fwd(*attn)
+
+
+@pytest.mark.parametrize("io", [_lib.RGLRU_IO_BF16, _lib.RGLRU_IO_F32])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (16, 4), (16, 16), (80, 2)])
+def test_a_workspace_for_a_capacity_serves_smaller_batches(io, dim, hq, hkv):
+    """A call of fewer tokens or sequences, or with a smaller bound on a sequence's new tokens, never needs more."""
+    for n in (1, 2, 5, 9, 16, 17, 40):
+        last = 0
+        for t in (1, 2, 5, 16, 17, 33, 64, 100, 333, 1000, 4096, 30000):
+            sizes = [glr.rglru_paged_attn_workspace_bytes(shape(n_tokens=t, n_seqs=m, q_heads=hq, kv_heads=hkv, head_dim=dim, io_dtype=io,
+                                                                max_new=new, max_pages=600))
+                     for m in range(1, n + 1) for new in (1, 2, 20, 300, 0)]
+            assert max(sizes[:-1] + [0]) <= sizes[-1] and last <= sizes[-1], (n, t)
+            last = sizes[-1]

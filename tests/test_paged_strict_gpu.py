@@ -112,3 +112,17 @@ def test_rows_aligned_to_16_bytes_and_no_more(gpu_lib, dtype, dim, new):
     assert q.data_ptr() % 32 == o.data_ptr() % 32 == 16 and q.stride(0) * q.element_size() % 32 == 16
     gpu_lib.rglru_paged_attn_fwd(q, b.d_k, b.d_v, b.d_table, b.d_cu, b.d_kv, o=o, lse=lse)
     b.check(o, lse)
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("hq,hkv", [(2, 1), (8, 8), (16, 4)])
+@pytest.mark.parametrize("n", [2, 6, 16, 19])
+def test_single_tokens_beside_chunks(gpu_lib, dtype, dim, hq, hkv, n):
+    """Batches on both sides of the rules by which the two kernels share a call, with the bound on new tokens and without it; in a
+    workspace of the largest call."""
+    new = [90 if i % 7 == 1 else 2 if i % 5 == 4 else 1 for i in range(n)]
+    b = StrictBatch([150 + 11 * i for i in range(n)], new, hq=hq, hkv=hkv, dim=dim, page=16, dtype=dtype, pad=5, seed=n)
+    ws = torch.full((160 << 20,), 255, dtype=torch.uint8, device="cuda")
+    for kw in (dict(max_new=90), dict(max_new=0), dict(max_new=b.q.shape[0])):
+        b.check(*b.call(gpu_lib, workspace=ws, **kw))
+    b.check(*b.call(gpu_lib, window=33, workspace=ws), window=33)
