@@ -118,7 +118,8 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *   o   = sum_j softmax_j(scale q . k_j) v_j        lse = ln sum_j exp(scale q . k_j)
  *
  * with q . k, scores, softmax and sums in float32, the scale applied to q . k. A row that sees no key (p < 0, or
- * all its scores -inf) gets o = 0 and lse = -inf. What a row does not see has
+ * all its scores -inf) gets o = 0 and lse = -inf; one with a score of +inf or
+ * NaN gets NaN in both. What a row does not see has
  * no influence on it, infinities and NaN included (at given lengths not on a
  * bit of it); padding rows of o and lse are left as they were. Weights of 2^-118
  * of a row's largest and less, the 0 of a score of -inf among them, may count as

@@ -126,3 +126,20 @@ def test_single_tokens_beside_chunks(gpu_lib, dtype, dim, hq, hkv, n):
     for kw in (dict(max_new=90), dict(max_new=0), dict(max_new=b.q.shape[0])):
         b.check(*b.call(gpu_lib, workspace=ws, **kw))
     b.check(*b.call(gpu_lib, window=33, workspace=ws), window=33)
+
+
+@pytest.mark.parametrize("dtype,dim", KINDS)
+@pytest.mark.parametrize("bad", [INF, NAN])
+@pytest.mark.parametrize("ctx,new", [(70, 1), (70, 60), (9000, 4), (9000, 60)])
+def test_scores_of_infinity_and_nan(gpu_lib, dtype, dim, bad, ctx, new):
+    """A score of +inf or NaN makes o and lse of its row NaN; rows that do not see that key are as without it."""
+    b = StrictBatch([ctx, 33], [new, new], hq=2, hkv=1, dim=dim, page=64, dtype=dtype, seed=dim + new)
+    b.q.copy_(b.q.abs() + 0.1)
+    b.d_q.copy_(b.q)
+    b.put(0, ctx + new // 2, k=bad)
+    b.put(0, 5, v=INF, dims=1)
+    o, lse = b.call(gpu_lib)
+    b.check(o, lse)
+    assert torch.isnan(o[new // 2:new]).all() and torch.isnan(lse[new // 2:new]).all()
+    b.put(1, 7, k=bad)            # out of every row's window
+    b.check(*b.call(gpu_lib, window=20), window=20)
