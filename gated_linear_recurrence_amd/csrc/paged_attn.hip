@@ -642,7 +642,7 @@ struct Line {
 // through its own LDS buffers without a barrier; the waves of a workgroup merge
 // at the end of a unit. What counts is how many bytes are in flight: a
 // wave asks for the next keys (values) as soon as it has read the buffer that
-// they go to. 64 sequences of up to 8192 keys, 8 key heads of 128 in bf16: 0.197
+// they go to. 64 sequences of up to 8192 keys, 8 key heads of 128 in bf16: 0.195
 // ms, 5.5 TB/s; of 32 768 keys: 6.1 TB/s.
 constexpr int kNarrowRows = 32, kNarrowKeys = 32, kNarrowOver = 6;
 
@@ -671,7 +671,7 @@ struct Narrow {
   // The one buffer holds four slices of columns, each loaded anew as soon as it is read: those of the values take the
   // place of those of the keys and the other way round. Half of the queries lie in LDS, as the registers would not hold
   // them and the output (float32, D = 256, 64 sequences of 8000 keys, 2 key heads: whole tiles in turn 3.9 TB/s, slices
-  // 4.4, with half of the queries in LDS 5.1).
+  // 4.4, with half of the queries in LDS 5.1, now that no register spills 5.7).
   static constexpr int kSlice = kBuffers == 1 ? D / 4 : D;
 };
 
@@ -705,10 +705,10 @@ __device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) 
 // Bound by the matrix cores. kRows rows of one (sequence, key head) share
 // every tile of kKeys keys and values, which the waves fetch together into one
 // of two LDS buffers while they work on the other; one barrier a tile. 2048
-// tokens after 30 011, 32 query and 8 key heads of 128: 0.92 to 0.99 ms by card, 1.1
+// tokens after 30 011, 32 query and 8 key heads of 128: 0.91 to 1.00 ms by card, 1.0 to 1.1
 // PFLOP/s, where an 8192^3 library product reaches 1.14 on the same card; the
 // matrix pipes are busy 53 % of the time at the 1.9 GHz that the power allows.
-// Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.55 to 0.58 ms,
+// Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.54 to 0.58 ms,
 // 0.9 PFLOP/s.
 template <typename E, int D>
 struct Wide {
@@ -717,7 +717,7 @@ struct Wide {
   // long, so less shows of the softmax: one wave per SIMD in a workgroup, half as many rows left idle
   static constexpr int kWaves = kBf16 ? 8 : 4;
   // Workgroups on a CU: two where the registers allow it (float32, D = 64), so that one's softmax runs beside the other's
-  // products (2048 tokens after 8000, 4 key heads: 378 -> 337 us), but one for calls whose stretches would be shorter than
+  // products (2048 tokens after 8000, 4 key heads: 378 -> 337 us, 307 now), but one for calls whose stretches would be shorter than
   // kShort tiles. 208 calls of 1 to 20 chunks of 50 to 1000 tokens after 0 to 2000, 2 to 8 key heads, timed with one and with two:
   // one is up to 1.3 times as fast at 1 to 3 tiles, the same at 8 to 12, two 1.1 times as fast from 20 on.
   static constexpr int kGroups = !kBf16 && D == 64 ? 2 : 1, kShort = 10;
