@@ -574,8 +574,9 @@ __device__ __forceinline__ void store4(uint8_t* p, float a, float b, float c, fl
   }
 }
 
-// The D outputs of one row times `f` (0 for a row without weights, whatever its sums are), 16 bytes per lane and instruction. The two half-waves hold 4 elements each of every
-// 8: for bf16 they trade, so that one has the 8 of an even group and the other those of the next.
+// The D outputs of one row times `f` (0 for a row without weights, whatever its sums are), 16 bytes per lane and
+// instruction. The two half-waves hold 4 elements each of every 8: for bf16 they trade, so that one has the 8 of an even
+// group and the other those of the next.
 template <typename E, int D>
 __device__ __forceinline__ void store_row(uint8_t* to, const f32x16* o, float f, int h) {
 #pragma unroll
@@ -707,7 +708,7 @@ __device__ __forceinline__ int32_t narrow_size(const AttnArgs& a, const Seq& s) 
 // of two LDS buffers while they work on the other; one barrier a tile. 2048
 // tokens after 30 011, 32 query and 8 key heads of 128: 0.91 to 1.00 ms by card, 1.0 to 1.1
 // PFLOP/s, where an 8192^3 library product reaches 1.14 on the same card; the
-// matrix pipes are busy 53 % of the time at the 1.9 GHz that the power allows.
+// matrix pipes are busy 54 % of the time at the 1.9 GHz that the power allows.
 // Eight prompts of 4096 with a window of 2048, 10 heads of 256: 0.54 to 0.58 ms,
 // 0.9 PFLOP/s.
 template <typename E, int D>
@@ -1155,9 +1156,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
       float pc[kAhead], pl[kAhead];
       float4 z[kAhead];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        fetch(min(i0 + k * step, pieces - 1), q, pc[k], pl[k], z[k]);
-      }
+      for (int k = 0; k < kAhead; ++k) fetch(min(i0 + k * step, pieces - 1), q, pc[k], pl[k], z[k]);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k)
         if (i0 + k * step < pieces) merge(c, l, acc, pc[k], pl[k], z[k]);
@@ -1406,8 +1405,7 @@ float log2_scale(float scale) { return std::fabs(scale) * kLog2e; }
 rglru_status_t check(const rglru_paged_shape_t& s) {
   if (!valid_pages(s) || !valid_table(s) || !valid_io(s) || s.kv_heads < 1 || s.q_heads < s.kv_heads ||
       s.q_heads > (1 << 14) || s.q_heads % s.kv_heads != 0 || s.n_tokens * s.q_heads > (int64_t(1) << 31) - (1 << 16) ||
-      s.head_dim < 1 || s.head_dim > (1 << 16) || s.window < 0 ||
-      !std::isfinite(log2_scale(s.scale)) ||
+      s.head_dim < 1 || s.head_dim > (1 << 16) || s.window < 0 || !std::isfinite(log2_scale(s.scale)) ||
       row_stride(s.q_stride, int64_t(s.q_heads) * s.head_dim) < 0)
     return RGLRU_ERR_INVALID_ARGUMENT;
   if (s.head_dim != 64 && s.head_dim != 128 && s.head_dim != 256) return RGLRU_ERR_UNSUPPORTED;

@@ -30,14 +30,16 @@ extern "C" {
 /* Limits beyond which a call returns RGLRU_ERR_INVALID_ARGUMENT (an entry
  * point checks the fields it reads): 0 <= n_tokens < 2^31; 1 <= n_seqs <=
  * 2^16; page_size a power of two from 8 to 1024; n_pages >= 1 with n_pages *
- * page_size < 2^31; max_pages >= 1 with max_pages * page_size <= 2^31 - 2^16; 1 <= kv_heads <= q_heads <= 2^14 with
- * q_heads a multiple of kv_heads; n_tokens * q_heads <= 2^31 - 2^16; head_dim >= 1;
- * io_dtype an rglru_io_t; max_new, window >= 0; |scale| <= 2.35e38 (times log2 e it
- * has to be finite); strides 0 or at least the dense row. Within them, a head_dim other than 64, 128 or 256
- * is RGLRU_ERR_UNSUPPORTED, and a stride that is not a multiple of 16 bytes
- * RGLRU_ERR_MISALIGNED. An output (what is updated in place and the workspace
- * too) that overlaps another one or an input is RGLRU_ERR_INVALID_ARGUMENT;
- * strided rows count from the first one's start to the last one's end. */
+ * page_size < 2^31; max_pages >= 1 with max_pages * page_size <= 2^31 -
+ * 2^16; 1 <= kv_heads <= q_heads <= 2^14 with q_heads a multiple of
+ * kv_heads; n_tokens * q_heads <= 2^31 - 2^16; head_dim >= 1; io_dtype an
+ * rglru_io_t; max_new, window >= 0; |scale| <= 2.35e38 (times log2 e it has
+ * to be finite); strides 0 or at least the dense row. Within them, a
+ * head_dim other than 64, 128 or 256 is RGLRU_ERR_UNSUPPORTED, and a stride
+ * that is not a multiple of 16 bytes RGLRU_ERR_MISALIGNED. An output (what
+ * is updated in place and the workspace too) that overlaps another one or an
+ * input is RGLRU_ERR_INVALID_ARGUMENT; strided rows count from the first
+ * one's start to the last one's end. */
 typedef struct {
   int64_t n_tokens;   /* T: rows of the packed batch (a capacity: rows from cu_seqlens[n_seqs] on are padding) */
   int64_t n_pages;    /* pages of the cache */
@@ -117,17 +119,18 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  *
  *   o   = sum_j softmax_j(scale q . k_j) v_j        lse = ln sum_j exp(scale q . k_j)
  *
- * with q . k, scores, softmax and sums in float32, the scale applied to q . k. A row that sees no key (p < 0, or
- * all its scores -inf) gets o = 0 and lse = -inf; one with a score of +inf or
- * NaN gets NaN in both. What a row does not see has
- * no influence on it, infinities and NaN included (at given lengths not on a
- * bit of it); padding rows of o and lse are left as they were. Weights of 2^-118
- * of a row's largest and less, the 0 of a score of -inf among them, may count as
- * nothing: a finite value adds nothing there, an infinite one gives infinity or
- * NaN. Sums are formed with weights up to 2^8 and divided at the end, so of n
- * visible values none should pass 3.4e38 / (2^8 n), or they may overflow. For
- * bf16 the softmax weights are rounded to bf16 where they enter the product with
- * the values (2^-8 relative at most). The same call gives the same bits each time.
+ * with q . k, scores, softmax and sums in float32, the scale applied to q . k.
+ * A row that sees no key (p < 0, or all its scores -inf) gets o = 0 and lse =
+ * -inf; one with a score of +inf or NaN gets NaN in both. What a row does not
+ * see has no influence on it, infinities and NaN included (at given lengths
+ * not on a bit of it); padding rows of o and lse are left as they were.
+ * Weights of 2^-118 of a row's largest and less, the 0 of a score of -inf
+ * among them, may count as nothing: a finite value adds nothing there, an
+ * infinite one gives infinity or NaN. Sums are formed with weights up to 2^8
+ * and divided at the end, so of n visible values none should pass 3.4e38 /
+ * (2^8 n), or they may overflow. For bf16 the softmax weights are rounded to
+ * bf16 where they enter the product with the values (2^-8 relative at most).
+ * The same call gives the same bits each time.
  *
  *   cu_seqlens       : [N + 1] int32 as above.       kv_lens : [N] int32, new tokens included.
  *   block_table      : [N, max_pages] int32; pages outside the cache give
