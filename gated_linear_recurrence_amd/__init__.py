@@ -18,10 +18,18 @@ from .ops import (  # noqa: F401
     rglru_delta_ckpt_elems,
     rglru_delta_rule_bwd,
     rglru_delta_rule_fwd,
+    rglru_page_compact,
+    rglru_page_copy,
+    rglru_page_fork,
+    rglru_page_free,
     rglru_page_plan,
     rglru_paged_attn_fwd,
+    rglru_paged_attn_q4_fwd,
+    rglru_paged_attn_q4_workspace_bytes,
     rglru_paged_attn_workspace_bytes,
+    rglru_paged_kv_read_q4,
     rglru_paged_kv_write,
+    rglru_paged_kv_write_q4,
     rglru_ckpt_elems,
     rglru_fwd,
     rglru_fwd_scratch,

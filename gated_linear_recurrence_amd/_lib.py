@@ -34,6 +34,7 @@ class rglru_shape_t(ctypes.Structure):
     ]
 
 
+RGLRU_PAGE_COPY_ARRAYS = 64
 RGLRU_DELTA_GDN = 0
 RGLRU_DELTA_KDA = 1
 
@@ -105,6 +106,16 @@ _SIGNATURES = {
     "rglru_paged_kv_write": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 6),
     "rglru_paged_attn_workspace_bytes": (c_size_t, [POINTER(rglru_paged_shape_t)]),
     "rglru_paged_attn_fwd": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 9 + [c_size_t, _vp]),
+    "rglru_paged_kv_write_q4": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 8),
+    "rglru_paged_kv_read_q4": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 8),
+    "rglru_paged_attn_q4_workspace_bytes": (c_size_t, [POINTER(rglru_paged_shape_t)]),
+    "rglru_paged_attn_q4_fwd": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 11 + [c_size_t, _vp]),
+    "rglru_page_fork": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 13),
+    "rglru_page_free_workspace_bytes": (c_size_t, [POINTER(rglru_paged_shape_t)]),
+    "rglru_page_free": (c_int, [POINTER(rglru_paged_shape_t)] + [_vp] * 9 + [c_size_t, _vp]),
+    "rglru_page_compact_workspace_bytes": (c_size_t, [POINTER(rglru_paged_shape_t)]),
+    "rglru_page_compact": (c_int, [POINTER(rglru_paged_shape_t), c_int64] + [_vp] * 13 + [c_size_t, _vp]),
+    "rglru_page_copy": (c_int, [c_int64, _vp, c_int64, _vp, c_int32, POINTER(_vp), POINTER(c_int64), _vp]),
     "rglru_status_string": (ctypes.c_char_p, [c_int]),
     "rglru_abi_version": (c_int, []),
 }

@@ -19,7 +19,7 @@ LIB_NAME = "librglru.so"
 ARCH = "gfx950"
 
 SOURCES = ["rglru_scan.hip", "rglru_proj.hip", "delta_rule.hip", "delta_chunk.hip", "delta_bwd.hip",
-           "paged_cache.hip", "paged_attn.hip"]
+           "paged_cache.hip", "paged_attn.hip", "paged_q4.hip", "paged_attn_q4.hip", "page_pool.hip"]
 
 FLAGS = [
     f"--offload-arch={ARCH}",

@@ -818,3 +818,268 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
              cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
              v_cache.data_ptr(), o.data_ptr(), _addr(lse), workspace.data_ptr(), workspace.numel())
     return o, lse
+
+
+def _q4_cache(k_codes, k_scales, v_codes, v_scales, device):
+    """Checks the four arrays of a 4-bit cache; returns its shape [n_pages, Hkv, page_size, D]."""
+    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+        raise ValueError("k_codes must be a tensor [n_pages, Hkv, page_size, D / 2]")
+    rows, dim = tuple(k_codes.shape[:3]), 2 * k_codes.shape[3]
+    if dim % 32 != 0:
+        raise ValueError(f"k_codes has rows of {dim // 2} bytes, expected a multiple of 16 (blocks of 32 elements)")
+    if max(rows[1], rows[2], dim) >> 31:
+        raise ValueError(f"k_codes has shape {tuple(k_codes.shape)}, expected heads, page size and width below 2^31")
+    _need(k_codes, "k_codes", (*rows, dim // 2), torch.uint8, device)
+    _need(v_codes, "v_codes", (*rows, dim // 2), torch.uint8, device)
+    _need(k_scales, "k_scales", (*rows, dim // 32), torch.uint8, device)
+    _need(v_scales, "v_scales", (*rows, dim // 32), torch.uint8, device)
+    return (*rows, dim)
+
+
+def rglru_paged_kv_write_q4(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
+                            v_codes: torch.Tensor, v_scales: torch.Tensor, slot_map: torch.Tensor) -> None:
+    """Writes rows of k and v [T, Hkv, D] into the slots slot_map [T] (int32; negative: skipped) of a 4-bit cache.
+
+    Codes are uint8 [n_pages, Hkv, page_size, D / 2] (element 2i of a row in the low half of byte i), scales uint8
+    [n_pages, Hkv, page_size, D / 32]: 32 elements share the smallest power of two 2^(byte - 127) that takes the largest
+    of them to 6 or less, and each is rounded to the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 times it, a half to the even
+    code. A block with an infinity or NaN reads as NaN. k and v: float32 or bfloat16, possibly slices of wider rows
+    (one stride for both)."""
+    lib = _lib.load()
+    if not isinstance(k_codes, torch.Tensor):
+        raise TypeError("k_codes must be a tensor")
+    dev = k_codes.device
+    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    if not isinstance(k, torch.Tensor) or k.dtype not in _IO:
+        raise ValueError("k must be a float32 or bfloat16 tensor")
+    t, row = _rows(k, "k", heads, dim, k.dtype, dev)
+    tv, row_v = _rows(v, "v", heads, dim, k.dtype, dev)
+    if tv != t or row_v != row:
+        raise ValueError("k and v must have the same rows")
+    _need(slot_map, "slot_map", (t,), torch.int32, dev)
+    shape = _paged_shape(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[k.dtype], 0, 0, 0.0, 0, row)
+    _call_on(dev, lib.rglru_paged_kv_write_q4, "rglru_paged_kv_write_q4", ctypes.byref(shape), k.data_ptr(), v.data_ptr(),
+             k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr())
+
+
+def rglru_paged_kv_read_q4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                           slot_map: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                           k: Optional[torch.Tensor] = None, v: Optional[torch.Tensor] = None):
+    """The values of the slots slot_map [T] (int32; negative: 0) of a 4-bit cache, exact in both types.
+
+    Returns (k, v), [T, Hkv, D] of `dtype` (float32 or bfloat16)."""
+    lib = _lib.load()
+    if not isinstance(k_codes, torch.Tensor):
+        raise TypeError("k_codes must be a tensor")
+    dev = k_codes.device
+    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    if dtype not in _IO:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
+        raise ValueError("slot_map must be a tensor [T]")
+    t = slot_map.numel()
+    _need(slot_map, "slot_map", (t,), torch.int32, dev)
+    k, v = (_out(x, name, (t, heads, dim), dtype, dev) for x, name in ((k, "k"), (v, "v")))
+    shape = _paged_shape(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[dtype], 0, 0, 0.0, 0, 0)
+    _call_on(dev, lib.rglru_paged_kv_read_q4, "rglru_paged_kv_read_q4", ctypes.byref(shape), k_codes.data_ptr(),
+             k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+@functools.lru_cache(maxsize=1024)
+def _paged_attn_q4_bytes(*fields) -> int:
+    return int(_lib.load().rglru_paged_attn_q4_workspace_bytes(ctypes.byref(_paged_shape(*fields))))
+
+
+def rglru_paged_attn_q4_workspace_bytes(shape: _lib.rglru_paged_shape_t) -> int:
+    return int(_lib.load().rglru_paged_attn_q4_workspace_bytes(ctypes.byref(shape)))
+
+
+def rglru_paged_attn_q4_fwd(q: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                            v_scales: torch.Tensor, block_table: torch.Tensor, cu_seqlens: torch.Tensor,
+                            kv_lens: torch.Tensor, *, max_new: int = 0, window: int = 0, scale: Optional[float] = None,
+                            want_lse: bool = True, o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None):
+    """rglru_paged_attn_fwd over a 4-bit cache (see rglru_paged_kv_write_q4): the same arguments, masks and outputs.
+
+    q [T, Hq, D] is float32 or bfloat16, whichever the cache was written from; D 64, 128 or 256. workspace: at least
+    rglru_paged_attn_q4_workspace_bytes bytes, as there. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding
+    rows are left as they were."""
+    lib = _lib.load()
+    if not isinstance(k_codes, torch.Tensor):
+        raise TypeError("k_codes must be a tensor")
+    dev = k_codes.device
+    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype not in _IO:
+        raise ValueError("q must be a float32 or bfloat16 tensor [T, Hq, D]")
+    hq = _int32("Hq", q.shape[1])
+    t, row = _rows(q, "q", hq, dim, q.dtype, dev)
+    n = _packed(cu_seqlens, dev)
+    _need(kv_lens, "kv_lens", (n,), torch.int32, dev)
+    width = _table(block_table, n, dev)
+    o = _out(o, "o", (t, hq, dim), q.dtype, dev)
+    if want_lse or lse is not None:
+        lse = _out(lse, "lse", (t, hq), torch.float32, dev)
+    sc = (1.0 / float(dim) ** 0.5) if scale is None else float(scale)
+    fields = (t, n_pages, n, width, page_size, hq, heads, dim, _IO[q.dtype], _int32("max_new", max_new),
+              _int32("window", window), sc, row, 0)
+    if workspace is None:
+        workspace = torch.empty(max(_paged_attn_q4_bytes(*fields), 1), dtype=torch.uint8, device=dev)
+    else:
+        _scratch(workspace, dev)
+    _call_on(dev, lib.rglru_paged_attn_q4_fwd, "rglru_paged_attn_q4_fwd", ctypes.byref(_paged_shape(*fields)),
+             cu_seqlens.data_ptr(), kv_lens.data_ptr(), block_table.data_ptr(), q.data_ptr(), k_codes.data_ptr(),
+             k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), o.data_ptr(), _addr(lse), workspace.data_ptr(),
+             workspace.numel())
+    return o, lse
+
+
+def _pool(block_table, lens, name, shares, free_pages, free_count, page_size):
+    """Checks the arrays of a page pool; returns its shape and device."""
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a tensor [N, max_pages]")
+    dev = block_table.device
+    n = _int32("the number of rows", block_table.shape[0])
+    width = _table(block_table, n, dev)
+    _need(lens, name, (n,), torch.int32, dev)
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be a tensor [n_pages]")
+    n_pages = free_pages.numel()
+    _need(free_pages, "free_pages", (n_pages,), torch.int32, dev)
+    _need(shares, "shares", (n_pages,), torch.int32, dev)
+    _need(free_count, "free_count", (1,), torch.int32, dev)
+    return _paged_shape(0, n_pages, n, width, _int32("page_size", page_size), 0, 0, 0, 0, 0, 0, 0.0, 0, 0), dev
+
+
+def _pool_outs(outs, names, sizes, device):
+    if outs.count(None) == len(outs):   # pieces of one allocation
+        return torch.empty(sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
+    return tuple(_out(o, k, (m,), torch.int32, device) for o, k, m in zip(outs, names, sizes))
+
+
+def _pool_scratch(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    _scratch(workspace, device)
+    return workspace
+
+
+def rglru_page_fork(fork_from: torch.Tensor, lens: torch.Tensor, block_table: torch.Tensor, shares: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int,
+                    held_lens: Optional[torch.Tensor] = None, pairs: Optional[torch.Tensor] = None,
+                    lens_out: Optional[torch.Tensor] = None, held_lens_out: Optional[torch.Tensor] = None,
+                    free_count_out: Optional[torch.Tensor] = None, unserved: Optional[torch.Tensor] = None):
+    """Rows of the block table go on from other rows' contexts (all int32): row n from row fork_from[n], if that is >= 0.
+
+    lens [N]: tokens of every row, 0 for a row that is to be forked; held_lens [N] (default: lens): tokens its pages
+    were taken for. block_table [N, max_pages] and shares [n_pages] (the rows that hold a page beyond the first) are
+    updated in place: full pages are shared, a last one that is not full gets a page from the stack free_pages, to be
+    filled by rglru_page_copy(pairs, caches). A row whose source is itself, forked in this call or not there, that is
+    not empty, or for which no page is left is not served and stays as it was.
+    Returns (pairs [N, 2]: from, to or -1, -1; lens_out [N]; held_lens_out [N]; free_count_out [1]; unserved [1])."""
+    lib = _lib.load()
+    shape, dev = _pool(block_table, lens, "lens", shares, free_pages, free_count, page_size)
+    n = shape.n_seqs
+    _need(fork_from, "fork_from", (n,), torch.int32, dev)
+    _opt(held_lens, "held_lens", (n,), torch.int32, dev)
+    names = ("lens_out", "held_lens_out", "free_count_out", "unserved")
+    if pairs is None and lens_out is None and held_lens_out is None and free_count_out is None and unserved is None:
+        pairs, lens_out, held_lens_out, free_count_out, unserved = torch.empty(
+            4 * n + 2, dtype=torch.int32, device=dev).split_with_sizes((2 * n, n, n, 1, 1))
+        pairs = pairs.view(n, 2)
+    else:
+        pairs = _out(pairs, "pairs", (n, 2), torch.int32, dev)
+        lens_out, held_lens_out, free_count_out, unserved = _pool_outs(
+            (lens_out, held_lens_out, free_count_out, unserved), names, (n, n, 1, 1), dev)
+    _call_on(dev, lib.rglru_page_fork, "rglru_page_fork", ctypes.byref(shape), fork_from.data_ptr(), lens.data_ptr(),
+             _addr(held_lens), block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+             pairs.data_ptr(), lens_out.data_ptr(), held_lens_out.data_ptr(), free_count_out.data_ptr(), unserved.data_ptr())
+    return pairs, lens_out, held_lens_out, free_count_out, unserved
+
+
+def rglru_page_free(keep_lens: torch.Tensor, held_lens: torch.Tensor, block_table: torch.Tensor, shares: torch.Tensor,
+                    free_pages: torch.Tensor, free_count: torch.Tensor, *, page_size: int,
+                    held_lens_out: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None):
+    """Rows give up the pages behind their first keep_lens [N] tokens of held_lens [N] (all int32; 0 ends a request).
+
+    shares [n_pages] and free_pages [n_pages] are updated in place: a page that other rows hold stays theirs, one
+    that nobody holds any more goes onto the stack, those of a call in descending order. workspace: a uint8 device tensor
+    of at least rglru_page_free_workspace_bytes bytes, allocated here when None; calls sharing one must not overlap.
+    Returns (held_lens_out [N], free_count_out [1])."""
+    lib = _lib.load()
+    shape, dev = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
+    n = shape.n_seqs
+    _need(keep_lens, "keep_lens", (n,), torch.int32, dev)
+    held_lens_out, free_count_out = _pool_outs((held_lens_out, free_count_out), ("held_lens_out", "free_count_out"), (n, 1), dev)
+    workspace = _pool_scratch(workspace, int(lib.rglru_page_free_workspace_bytes(ctypes.byref(shape))), dev)
+    _call_on(dev, lib.rglru_page_free, "rglru_page_free", ctypes.byref(shape), keep_lens.data_ptr(), held_lens.data_ptr(),
+             block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+             held_lens_out.data_ptr(), free_count_out.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return held_lens_out, free_count_out
+
+
+def rglru_page_compact(held_lens: torch.Tensor, block_table: torch.Tensor, shares: torch.Tensor, free_pages: torch.Tensor,
+                       free_count: torch.Tensor, *, page_size: int, keep_pages: int,
+                       block_table_out: Optional[torch.Tensor] = None, shares_out: Optional[torch.Tensor] = None,
+                       free_pages_out: Optional[torch.Tensor] = None, free_count_out: Optional[torch.Tensor] = None,
+                       pairs: Optional[torch.Tensor] = None, n_pairs: Optional[torch.Tensor] = None,
+                       unmoved: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The pool shrinks to its first keep_pages pages: pages in use behind them move to free ones before (all int32).
+
+    held_lens [N] says which columns of block_table [N, max_pages] name pages in use. Nothing is updated in place; the
+    contents follow by rglru_page_copy(pairs, caches, n_pairs=n_pairs). workspace: at least
+    rglru_page_compact_workspace_bytes bytes, as for rglru_page_free.
+    Returns (block_table_out, shares_out, free_pages_out [n_pages]: the free pages before keep_pages in descending order,
+    then -1; free_count_out [1]; pairs [min(keep_pages, n_pages - keep_pages), 2]: from, to, then -1; n_pairs [1];
+    unmoved [1]: pages in use behind keep_pages that found no place)."""
+    lib = _lib.load()
+    shape, dev = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
+    n_pages, keep = shape.n_pages, _int32("keep_pages", keep_pages)
+    if keep > n_pages:
+        raise ValueError(f"keep_pages is {keep}, expected at most {n_pages}")
+    room = min(keep, n_pages - keep)
+    block_table_out = _out(block_table_out, "block_table_out", (shape.n_seqs, shape.max_pages), torch.int32, dev)
+    pairs = _out(pairs, "pairs", (room, 2), torch.int32, dev)
+    shares_out, free_pages_out, free_count_out, n_pairs, unmoved = _pool_outs(
+        (shares_out, free_pages_out, free_count_out, n_pairs, unmoved),
+        ("shares_out", "free_pages_out", "free_count_out", "n_pairs", "unmoved"), (n_pages, n_pages, 1, 1, 1), dev)
+    workspace = _pool_scratch(workspace, int(lib.rglru_page_compact_workspace_bytes(ctypes.byref(shape))), dev)
+    _call_on(dev, lib.rglru_page_compact, "rglru_page_compact", ctypes.byref(shape), keep, held_lens.data_ptr(),
+             block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+             block_table_out.data_ptr(), shares_out.data_ptr(), free_pages_out.data_ptr(), free_count_out.data_ptr(),
+             pairs.data_ptr() if room else None, n_pairs.data_ptr(), unmoved.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return block_table_out, shares_out, free_pages_out, free_count_out, pairs, n_pairs, unmoved
+
+
+@functools.lru_cache(maxsize=256)
+def _page_bytes(sizes):
+    return (ctypes.c_int64 * len(sizes))(*sizes)
+
+
+def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tensor] = None) -> None:
+    """Copies page pairs[i, 0] to page pairs[i, 1] of every cache, for the pairs [M, 2] (int32; negative: skipped).
+
+    caches: contiguous tensors [n_pages, ...] of any type, a page of each a multiple of 16 bytes: the keys and values of
+    every layer under one block table. n_pairs [1]: the pairs to look at, on the GPU (default: all). No page is the
+    target of two pairs, or the source of one and the target of another."""
+    lib = _lib.load()
+    caches = list(caches)
+    if not caches or not all(isinstance(c, torch.Tensor) and c.dim() >= 1 and c.shape[0] > 0 for c in caches):
+        raise ValueError("caches must be tensors [n_pages, ...]")
+    dev, n_pages = caches[0].device, caches[0].shape[0]
+    if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs must be a tensor [M, 2]")
+    m = _int32("the number of pairs", pairs.shape[0])
+    _need(pairs, "pairs", (m, 2), torch.int32, dev)
+    _opt(n_pairs, "n_pairs", (1,), torch.int32, dev)
+    sizes = []
+    for c in caches:
+        if c.device != dev or c.shape[0] != n_pages or not c.is_contiguous():
+            raise ValueError(f"caches must be contiguous, on {dev}, with {n_pages} pages")
+        sizes.append(c.numel() // n_pages * c.element_size())
+    for i in range(0, len(caches), _lib.RGLRU_PAGE_COPY_ARRAYS):
+        part = caches[i: i + _lib.RGLRU_PAGE_COPY_ARRAYS]
+        arrays = (ctypes.c_void_p * len(part))(*[c.data_ptr() for c in part])
+        _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", _int32("n_pages", n_pages, 1), pairs.data_ptr() if m else None, m,
+                 _addr(n_pairs), len(part), arrays, _page_bytes(tuple(sizes[i: i + len(part)])))
