@@ -40,7 +40,7 @@ struct Narrow {
   // values (and there are two workgroups at 4 KB), at 16 KB one of each, at 32 KB one for both. kGroups also tells
   // the compiler how many waves share a SIMD: with two it keeps the output out of the accumulation registers, which it
   // copies to and fro otherwise (D = 64: 22.4 -> 21 us for 16 sequences of 2000 keys).
-  static constexpr int kWaves = 4;
+  static constexpr int kWaves = 4, kStretches = 1;
   static constexpr int kBuffers = kTileBytes <= 8192 ? 4 : 32768 / kTileBytes;
   static constexpr int kGroups = kTileBytes == 4096 ? 2 : 1;
   static constexpr int kThreads = kWaves * 64;

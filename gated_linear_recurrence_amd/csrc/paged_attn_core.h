@@ -233,9 +233,10 @@ struct Tile {
 
 // What one kernel leaves for the join.
 struct Cuts {
-  int32_t* joins;  // [grid][4]: sequence, key head, pieces (0: none) and first row of what the cut before workgroup b parted
-  float* parts;    // [grid][2]: partial results of a workgroup's first and last unit
-  int32_t grid;
+  int32_t* joins;  // [grid][4]: sequence, key head, pieces (0: none) and first row of what the cut before stretch b parted; or
+                   // [N * Hkv][2], by unit: pieces (0: none) and the stretch that the first cut is before
+  float* parts;    // [grid][2]: partial results of a stretch's first and last unit
+  int32_t grid;    // stretches
 };
 
 struct RowTile;
@@ -841,29 +842,22 @@ __global__ __launch_bounds__(kSchedThreads) void sched_kernel(AttnArgs a) {
 // Merges the pieces of every unit that was cut, in the order of the keys. A
 // row takes D / 4 threads; the other threads of a workgroup take further rows
 // or, where there are many pieces, further pieces of the same row.
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kManyPieces = 64;
 
-template <typename E, int D, int kWideRows>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide_share, int narrow_share) {
-  constexpr int kLanes = D / 4, kSets = kJoinThreads / kLanes, kAhead = 8, kShare = 16;
+// Share y of `shares` of the rows from r0 on of one unit, whose second piece is that of stretch b; kCols columns from d0 on.
+template <typename E, int D, int kCols = D>
+__device__ __forceinline__ void join_unit(const AttnArgs& a, const Cuts& cuts, int kRows, int b, int pieces, int n, int hk, int r0,
+                                          int y, int shares, int d0 = 0) {
+  constexpr int kLanes = kCols / 4, kSets = kJoinThreads / kLanes, kAhead = 8, kShare = 16;
   __shared__ float4 acc_s[kSets][kLanes];
   __shared__ float l_s[kSets], c_s[kSets];
-  // workgroups: `wide_share` for each cut of the wide kernel, then `narrow_share` for each of the narrow one
-  const int wide_blocks = a.wide.grid * wide_share;
-  const bool wide = int(blockIdx.x) < wide_blocks;
-  const Cuts& cuts = wide ? a.wide : a.narrow;
-  const int at = wide ? blockIdx.x : blockIdx.x - wide_blocks, shares = wide ? wide_share : narrow_share;
-  const int b = at / shares, y = at - b * shares, tid = threadIdx.x;
-  const int pieces = cuts.joins[4 * b + 2];
-  if (pieces == 0) return;
-  const int n = cuts.joins[4 * b], hk = cuts.joins[4 * b + 1], r0 = cuts.joins[4 * b + 3];
+  const int tid = threadIdx.x;
   const Seq s = seq_of(a, n);
-  const int kRows = wide ? kWideRows : kNarrowRows;
   const int64_t part_size = int64_t(kRows) * (D + 2);
   const int rows = min(kRows, s.fresh * a.group - r0);
   // The sets share a row's pieces where there are many and that takes fewer reads in a row than a set per row.
   const bool share = pieces > kShare && (rows + shares - 1) / shares * kAhead < pieces;
-  const int set = tid / kLanes, d = (tid % kLanes) * 4;
+  const int set = tid / kLanes, d = d0 + (tid % kLanes) * 4;
   auto write = [&](int q, float c, float l, float4 acc) {
     const float inv = c == -INFINITY ? 0.0f : 1.0f / l;
     if (c == -INFINITY) acc = {0, 0, 0, 0};
@@ -907,7 +901,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
       continue;
     }
     acc_s[set][tid % kLanes] = acc;
-    if (d == 0) l_s[set] = l, c_s[set] = c;
+    if (tid % kLanes == 0) l_s[set] = l, c_s[set] = c;
     __syncthreads();
     if (set == 0) {
       c = -INFINITY, l = 0.0f;
@@ -918,6 +912,40 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
     }
     __syncthreads();
   }
+}
+
+template <typename E, int D, int kWideRows, bool kByUnit = false>
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide_share, int narrow_share) {
+  // workgroups: `wide_share` for each cut of the wide kernel, then `narrow_share` for each of the narrow one (kByUnit: each unit)
+  const int wide_blocks = a.wide.grid * wide_share;
+  const bool wide = int(blockIdx.x) < wide_blocks;
+  const Cuts& cuts = wide ? a.wide : a.narrow;
+  const int64_t at = wide ? blockIdx.x : blockIdx.x - wide_blocks;
+  const int shares = wide ? wide_share : narrow_share;
+  if (kByUnit && !wide) {
+    // a unit that the narrow kernel has worked on has its entry
+    for (int64_t i = at; i < int64_t(a.N) * a.Hkv * shares; i += gridDim.x - wide_blocks) {
+      const int64_t unit = i / shares;
+      const int n = int(unit / a.Hkv), hk = int(unit - int64_t(n) * a.Hkv);
+      const int pieces = cuts.joins[2 * unit], b = cuts.joins[2 * unit + 1];   // asked for beside the lengths
+      const int64_t rows = int64_t(seq_of(a, n).fresh) * a.group;
+      if (rows == 0 || rows > kNarrowRows || pieces == 0) continue;
+      const int y = int(i - unit * shares);
+      if (pieces <= kManyPieces) {
+        join_unit<E, D>(a, cuts, kNarrowRows, b, pieces, n, hk, 0, y, shares);
+      } else {
+        // 32 columns of a row at a time, so that more threads share its pieces
+        for (int v = y; v < int(rows) * (D / 32); v += shares)
+          join_unit<E, D, 32>(a, cuts, kNarrowRows, b, pieces, n, hk, 0, v / (D / 32), kNarrowRows, v % (D / 32) * 32);
+      }
+    }
+    return;
+  }
+  const int b = int(at) / shares, y = int(at) - b * shares;
+  const int pieces = cuts.joins[4 * b + 2];
+  if (pieces == 0) return;
+  join_unit<E, D>(a, cuts, wide ? kWideRows : kNarrowRows, b, pieces, cuts.joins[4 * b], cuts.joins[4 * b + 1], cuts.joins[4 * b + 3],
+                  y, shares);
 }
 
 constexpr int kSlackPart = 32;  // a cut moves by up to this part of a stretch (an eighth of it to a 64th measured the same)
@@ -1194,7 +1222,7 @@ int64_t most_few(const rglru_paged_shape_t& s) {
 // call of fewer tokens would run it, so one of the largest size serves all.
 struct Plan {
   bool narrow, wide, own_list;
-  int narrow_grid, wide_grid;  // workgroups; of the wide kernel a multiple of 8
+  int narrow_grid, wide_grid;  // stretches: workgroups (of the wide kernel a multiple of 8) or their waves
   int64_t max_tiles;           // row tiles of the wide kernel at most
   size_t narrow_joins, narrow_parts, wide_joins, wide_parts, row_tiles, sched, bytes;  // offsets and size of the workspace
 };
@@ -1220,8 +1248,9 @@ Plan plan_of(const rglru_paged_shape_t& s, int narrow_keys, int few_units) {
     return int(units >= most || tiles >= most || units * tiles >= most ? most : units * tiles > 0 ? units * tiles : 1);
   };
   if (room) {
-    p.narrow_grid = grid_of(256 * N::kGroups, seqs * s.kv_heads, ceil_div(ceil_div(keys, narrow_keys), N::kWaves));
-    p.narrow_joins = take(size_t(p.narrow_grid) * 16);
+    p.narrow_grid = grid_of(256 * N::kGroups, seqs * s.kv_heads, ceil_div(ceil_div(keys, narrow_keys), N::kWaves)) * N::kStretches;
+    const size_t units = size_t(s.n_seqs) * s.kv_heads;
+    p.narrow_joins = take(N::kStretches > 1 ? units * 8 : size_t(p.narrow_grid) * 16);
     p.narrow_parts = take(size_t(p.narrow_grid) * 2 * part_floats<D>(kNarrowRows) * 4);
   }
   if (p.wide) {
@@ -1251,13 +1280,22 @@ void lay_out(AttnArgs& a, const Plan& p, uint8_t* workspace) {
   a.least_rows = p.narrow ? kNarrowRows : 0;
 }
 
-template <typename E, int D, typename W>
+template <typename E, int D, typename W, bool kByUnit = false>
 void join(const rglru_paged_shape_t& s, const AttnArgs& a, const Plan& p, hipStream_t st) {
   // A pass over kPass rows costs the latency of its reads, 2 to 3 us: one pass (rows of few pieces; with many, a row a pass).
   constexpr int kPass = kJoinThreads * 4 / D;
-  const int wide_share = W::kRows / kPass, narrow_share = int(p.wide ? ceil_div(kNarrowRows, kPass) : most_rows(s));
-  join_kernel<E, D, W::kRows><<<unsigned(p.wide_grid * wide_share + p.narrow_grid * narrow_share), kJoinThreads, 0, st>>>(
-      a, wide_share, narrow_share);
+  const int wide_share = W::kRows / kPass;
+  int narrow_share = int(p.wide ? ceil_div(kNarrowRows, kPass) : most_rows(s));
+  int64_t narrow = !kByUnit ? p.narrow_grid : p.narrow ? int64_t(s.n_seqs) * s.kv_heads : 0;
+  if (kByUnit && !p.wide && narrow > 0) {
+    // few units have many pieces each: more workgroups for a unit's rows
+    const int64_t pass = ceil_div(most_rows(s), kPass), spread = ceil_div(4 * kCus, narrow), most = most_rows(s) * (D / 32);
+    narrow_share = int(spread < pass ? pass : spread < most ? spread : most);
+  }
+  narrow *= narrow_share;
+  if (kByUnit && narrow > (1 << 20)) narrow = 1 << 20;   // they take further units in turn
+  join_kernel<E, D, W::kRows, kByUnit><<<unsigned(p.wide_grid * wide_share + narrow), kJoinThreads, 0, st>>>(a, wide_share,
+                                                                                                       narrow_share);
 }
 
 void set_args(AttnArgs& a, const rglru_paged_shape_t& s, const int32_t* cu_seqlens, const int32_t* kv_lens,

@@ -23,6 +23,7 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
@@ -102,7 +103,7 @@ struct Staged {
 // into the weights, a set of weights per block of columns: exact, and a value that is
 // not finite stays out of the products of rows that do not see it, as codes are
 // always finite.
-constexpr int kFewKeys = 64, kFewOver = 4;
+constexpr int kFewKeys = 64, kFewOver = 1;
 
 template <typename E>
 struct Few {
@@ -112,6 +113,28 @@ template <>
 struct Few<float> {
   typedef Split type;
 };
+
+// Weight i of an operand: 0 for one of 0.
+__device__ __forceinline__ uint32_t weight_bits(const Frag<uint16_t>& f, int i) { return f.w[i / 2] >> (16 * (i % 2)) & 0xFFFFu; }
+__device__ __forceinline__ uint32_t weight_bits(const Split& f, int i) { return f.w[0][i / 2] >> (16 * (i % 2)) & 0xFFFFu; }
+
+// top - 128 e, a pair at a time (the compiler takes a shift and a subtraction instead).
+__device__ __forceinline__ u16x2 exponents_below(u16x2 e, uint32_t top) {
+  uint32_t r;
+  asm("v_pk_mad_u16 %0, %1, %2, %3" : "=v"(r) : "v"(__builtin_bit_cast(uint32_t, e)), "v"(0xFF80FF80u), "s"(top));
+  return __builtin_bit_cast(u16x2, r);
+}
+// Word w of an operand with its exponents lowered, down to 0.
+__device__ __forceinline__ uint32_t lower(uint32_t x, u16x2 less) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, x), less));
+}
+__device__ __forceinline__ void lower(Frag<uint16_t>& to, const Frag<uint16_t>& from, int w, u16x2 less) {
+  to.w[w] = lower(from.w[w], less);
+}
+__device__ __forceinline__ void lower(Split& to, const Split& from, int w, u16x2 less) {
+#pragma unroll
+  for (int j = 0; j < 3; ++j) to.w[j][w] = lower(from.w[j][w], less);
+}
 
 __device__ __forceinline__ f32x4 mma16(const u32x4& a, const Frag<uint16_t>& b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b.w), c, 0, 0, 0);
@@ -124,20 +147,23 @@ __device__ __forceinline__ f32x4 mma16(const u32x4& a, const Split& b, f32x4 c) 
 }
 
 // A tile of 64 keys in LDS: codes of the keys, of the values, scales of the keys, of the values. Rows of kP pieces of 16 bytes;
-// piece c of row r lies at column c ^ swz(r), so that the lanes that one LDS cycle serves fall on different banks.
-template <typename E, int D>
+// piece c of row r lies at column c ^ swz(r), so that the lanes that one LDS cycle serves fall on different banks: rows
+// 16 j .. 16 j + 15 at one piece (keys), and rows 16 j + 4 g + i of one g at one piece (values).
+template <typename E, int D, int kSets>
 struct Narrow4 {
   static constexpr int kP = D / 32;
   static constexpr int kCodes = kFewKeys * D / 2, kScales = kFewKeys * kP;   // bytes
-  static constexpr int kTileBytes = 2 * kCodes + 2 * ((kScales + 255) / 256 * 256);
   static constexpr int kCodeLoads = kCodes / 1024, kScaleLoads = (kScales + 255) / 256, kLoads = kCodeLoads + kScaleLoads;
   static constexpr int kScaleBytes = kScaleLoads * 256;
+  static constexpr int kTileBytes = 2 * kCodes + 2 * kScaleBytes;
   static constexpr int kLoadRows = 64 / kP;   // rows that one load of codes fetches
-  static constexpr int kWaves = 4, kThreads = kWaves * 64, kBuffers = 2;
-  static constexpr int kGroups = D == 256 ? 1 : 2;   // workgroups on a CU
-  __device__ static constexpr int swz_k(int r) { return r / (16 / kP) & (kP - 1); }
-  __device__ static constexpr int swz_v(int r) {
-    return kP == 8 ? (r >> 1 & 1) | (r >> 4 & 3) << 1 : r >> 4 & (kP - 1);
+  static constexpr int kWaves = 4, kThreads = kWaves * 64, kStretches = kWaves;
+  // Workgroups on a CU, as many as the registers allow without spills.
+  static constexpr int kGroups = D == 256 || (D == 128 && kSets == 2 && sizeof(E) == 4) ? 1 : D == 64 && kSets == 1 ? 3 : 2;
+  // Pages of 8 keys each, looked up two tiles ahead.
+  static constexpr int kSegs = kFewKeys / kSeg, kRing = 2, kPageBytes = kRing * kSegs * 4;
+  __device__ static constexpr int swz(int r) {
+    return kP == 2 ? (r >> 3 ^ r >> 4) & 1 : kP == 4 ? (r >> 2 ^ r >> 4) & 3 : (r >> 1 & 1) | ((r >> 2 ^ r >> 4) & 3) << 1;
   }
 };
 
@@ -147,17 +173,6 @@ __device__ __forceinline__ void load_lds16(uint32_t to, const uint8_t* from) {
 }
 __device__ __forceinline__ void load_lds4(uint32_t to, const uint8_t* from) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(to), "v"(from) : "memory");
-}
-
-// v[i] of n, chosen by the lane: n is a power of two.
-template <int n>
-__device__ __forceinline__ int64_t choose(const int64_t* v, int i) {
-  if constexpr (n == 1) {
-    return v[0];
-  } else {
-    const int64_t lo = choose<n / 2>(v, i), hi = choose<n / 2>(v + n / 2, i);
-    return i & (n / 2) ? hi : lo;
-  }
 }
 
 __device__ __forceinline__ float quarter_max(float x) {
@@ -171,78 +186,128 @@ __device__ __forceinline__ float quarter_sum(float x) {
   return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
+// A wave's bound on the scales of its values: from kSpan below it on up to itself they pass as weights' exponents.
+constexpr int kSpan = 100;
+
+// Whether a key's scales (byte by byte) lie within the span.
+template <int kP>
+__device__ __forceinline__ bool within(const uint32_t* w, int ref) {
+  const u16x2 top = {uint16_t(ref), uint16_t(ref)};
+  u16x2 far = 0;
+#pragma unroll
+  for (int i = 0; i < (kP + 3) / 4; ++i) {
+    far = __builtin_elementwise_max(far, top - __builtin_bit_cast(u16x2, w[i] & 0x00FF00FFu));
+    far = __builtin_elementwise_max(far, top - __builtin_bit_cast(u16x2, w[i] >> 8 & 0x00FF00FFu));
+  }
+  return max(far[0], far[1]) <= kSpan;
+}
+
 // kSets sets of 16 rows of one wave.
 template <typename E, int D, int kSets>
 struct Wave4 {
-  using P = Narrow4<E, D>;
+  using P = Narrow4<E, D, kSets>;
   using O = typename Few<E>::type;
   O q[kSets][D / 32];
   f32x4 o[kSets][D / 16];
   float m[kSets], c[kSets], l[kSets];   // as in Wave
   int32_t lo[kSets], hi[kSets];
 
-  // This lane's share of the queries of row r: elements (D / 4) g on.
-  __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, int hk, int32_t rows, int lane) {
-    const int g = lane >> 4;
-    const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? O::kSigns : 0u;
+  // This lane's share of the queries of its rows, elements (D / 4) g on, as they lie in memory ..
+  struct Raw {
+    u32x4 w[kSets][D / 32 * int(sizeof(E)) / 2];
+  };
+  __device__ __forceinline__ Raw queries(const AttnArgs& a, const Seq& s, int hk, int32_t rows, int lane) const {
+    Raw raw;
 #pragma unroll
     for (int z = 0; z < kSets; ++z) {
       const int32_t r = z * 16 + (lane & 15);
       const bool live = r < rows;
       const int32_t t = live ? r / a.group : 0, head = live ? r - t * a.group : 0;
       const u32x4* const src = reinterpret_cast<const u32x4*>(
-          a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + head) * D + g * (D / 4)) * sizeof(E));
+          a.q + ((s.start + t) * a.q_stride + int64_t(hk * a.group + head) * D + (lane >> 4) * (D / 4)) * sizeof(E));
+#pragma unroll
+      for (int x = 0; x < D / 32 * int(sizeof(E)) / 2; ++x) {
+        raw.w[z][x] = 0;
+        if (live) raw.w[z][x] = src[x];
+      }
+    }
+    return raw;
+  }
+  // .. and as operands.
+  __device__ __forceinline__ void start(const AttnArgs& a, const Seq& s, const Raw& raw, int32_t rows, int lane) {
+    const uint32_t keep = a.q_sign == 0 ? 0u : ~0u, flip = a.q_sign < 0 ? O::kSigns : 0u;
+#pragma unroll
+    for (int z = 0; z < kSets; ++z) {
+      const int32_t r = z * 16 + (lane & 15);
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
-        const u32x4 none = 0;
-        if constexpr (sizeof(E) == 2) q[z][x].w = live ? src[x] : none;
-        else q[z][x] = split_query(live ? src[2 * x] : none, live ? src[2 * x + 1] : none);
+        if constexpr (sizeof(E) == 2) q[z][x].w = raw.w[z][x];
+        else q[z][x] = split_query(raw.w[z][2 * x], raw.w[z][2 * x + 1]);
         if (a.q_sign <= 0) set_bits(q[z][x], keep, flip);
       }
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) o[z][x] = 0.0f;
       m[z] = c[z] = -INFINITY;
       l[z] = 0.0f;
-      hi[z] = live ? max(s.kv - s.fresh + r / a.group, -1) : -1;
+      hi[z] = r < rows ? max(s.kv - s.fresh + r / a.group, -1) : -1;
       lo[z] = a.window > 0 ? max(hi[z] - a.window + 1, 0) : 0;
     }
   }
 
+  // A lane's share of keys 16 j + lane % 16: codes and powers.
+  struct Keys {
+    uint32_t w[D / 32];
+    float power[(D + 127) / 128];
+  };
+  // Where a lane's share of keys 0 .. 15 lies in a tile; that of keys 16 j on lies at an XOR of j, as swz is linear over XOR.
+  __device__ __forceinline__ static int keys_at(int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    if constexpr (D == 64) return r * (D / 2) + ((g >> 1) ^ P::swz(r)) * 16 + (g & 1) * 8;
+    else return r * (D / 2) + ((g * (D / 128)) ^ P::swz(r)) * 16;
+  }
+  __device__ __forceinline__ static Keys keys_of(const lds_u8* codes, const lds_u8* scales, int j, int at, int lane) {
+    const int from = (at ^ (P::swz(16 * j) * 16)) + 16 * j * (D / 2), g = lane >> 4;
+    const lds_u8* const sc = scales + (16 * j + (lane & 15)) * P::kP;
+    Keys k;
+    if constexpr (D == 64) {
+      const u32x2 x = *(const __attribute__((address_space(3))) u32x2*)(codes + from);
+      k.w[0] = x[0], k.w[1] = x[1];
+      k.power[0] = __uint_as_float(uint32_t(sc[g >> 1]) << 23);
+    } else {
+#pragma unroll
+      for (int h = 0; h < D / 128; ++h) {
+        const u32x4 x = *(const lds_u32x4*)(codes + (from ^ (h * 16)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k.w[4 * h + i] = x[i];
+        k.power[h] = __uint_as_float(uint32_t(sc[g * (D / 128) + h]) << 23);
+      }
+    }
+    return k;
+  }
+
   // Scores of the 64 keys in LDS: s[z][j] are keys 16 j + 4 g .. of the tile.
   __device__ __forceinline__ void scores(const lds_u8* codes, const lds_u8* scales, int lane, f32x4 (*s)[4]) const {
-    const int row = lane & 15, g = lane >> 4;
+    int at = keys_at(lane);
+    fresh_value(at);
+    Keys next = keys_of(codes, scales, 0, at, lane);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int r = 16 * j + row;
-      const lds_u8* const at = codes + r * (D / 2);
-      uint32_t w[D / 32];
-      float power[(D + 127) / 128];
-      if constexpr (D == 64) {
-        const u32x2 x = *(const __attribute__((address_space(3))) u32x2*)(at + ((g >> 1) ^ P::swz_k(r)) * 16 + (g & 1) * 8);
-        w[0] = x[0], w[1] = x[1];
-        power[0] = __uint_as_float(uint32_t(scales[r * P::kP + (g >> 1)]) << 23);
-      } else {
-#pragma unroll
-        for (int h = 0; h < D / 128; ++h) {
-          const u32x4 x = *(const lds_u32x4*)(at + ((g * (D / 128) + h) ^ P::swz_k(r)) * 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[4 * h + i] = x[i];
-          power[h] = __uint_as_float(uint32_t(scales[r * P::kP + g * (D / 128) + h]) << 23);
-        }
-      }
+      const Keys now = next;
+      if (j < 3) next = keys_of(codes, scales, j + 1, at, lane);
 #pragma unroll
       for (int z = 0; z < kSets; ++z) s[z][j] = 0.0f;
 #pragma unroll
       for (int x = 0; x < D / 32; ++x) {
-        const u32x4 k = values_of(w[x], power[x / 4]);
+        const u32x4 k = values_of(now.w[x], now.power[x / 4]);
 #pragma unroll
         for (int z = 0; z < kSets; ++z) s[z][j] = mma16(k, q[z][x], s[z][j]);
       }
+      order();
     }
   }
 
   // Turns the scores of set z into weights; `full`: every row of the wave sees all 64 keys.
-  __device__ __forceinline__ void weights(const AttnArgs& a, int z, f32x4* s, int32_t kv0, bool full, int lane) {
+  __device__ __forceinline__ void weights(float scale2, int z, f32x4* s, int32_t kv0, bool full, int lane) {
     const int g = lane >> 4;
     if (!full) {
 #pragma unroll
@@ -260,9 +325,9 @@ struct Wave4 {
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[j][i]);
     top = quarter_max(top);
     // the wave branches together, each row decides for itself: what other rows see must not change its bits
-    const bool grow = top * a.scale2 > c[z] + kSlack;
+    const bool grow = top * scale2 > c[z] + kSlack;
     if (__any(grow)) {
-      const float m_new = grow ? fmaxf(m[z], top) : m[z], c_new = m_new * a.scale2;
+      const float m_new = grow ? fmaxf(m[z], top) : m[z], c_new = m_new * scale2;
       const float keep = grow && c[z] != -INFINITY ? __builtin_amdgcn_exp2f(c[z] - c_new) : 1.0f;
       if (__any(keep != 1.0f)) {
 #pragma unroll
@@ -278,73 +343,107 @@ struct Wave4 {
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], a.scale2, -base));
+        s[j][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[j][i], scale2, -base));
         sum += s[j][i];
       }
     l[z] += sum;
   }
 
-  // Adds 64 weighted values to the output. kOdd: a block among them is NaN.
-  template <bool kOdd>
-  __device__ __forceinline__ void values(const lds_u8* codes, const lds_u8* scales, int lane, const f32x4 (*s)[4]) {
-    const int row = lane & 15, g = lane >> 4;
-    const int r = 16 * (row >> 2) + 4 * g + (row & 3);   // the row whose codes this lane hands to the others
-    // the scales of keys 16 j + 4 g ..: 4 kP bytes each
-    uint32_t sc[4][P::kP];
+  // The scales of keys 16 j + 4 g + i: byte i kP + b of sc[j].
+  struct Scales {
+    uint32_t w[4][P::kP];
+  };
+  __device__ __forceinline__ static Scales scales_of(const lds_u8* scales, int lane) {
+    Scales sc;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const lds_u8* const at = scales + (16 * j + 4 * g) * P::kP;
+      const lds_u8* const at = scales + (16 * j + 4 * (lane >> 4)) * P::kP;
       if constexpr (P::kP == 2) {
         const u32x2 x = *(const __attribute__((address_space(3))) u32x2*)at;
-        sc[j][0] = x[0], sc[j][1] = x[1];
+        sc.w[j][0] = x[0], sc.w[j][1] = x[1];
       } else {
 #pragma unroll
         for (int h = 0; h < P::kP / 4; ++h) {
           const u32x4 x = *(const lds_u32x4*)(at + 16 * h);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[j][4 * h + i] = x[i];
+          for (int i = 0; i < 4; ++i) sc.w[j][4 * h + i] = x[i];
         }
       }
     }
+    return sc;
+  }
+
+  // Codes of 16 keys in column 16 x + lane % 16; `at`: where the row lies whose codes this lane hands to the others.
+  __device__ __forceinline__ static int rows_at(int lane) {
+    const int i = lane & 15, r = 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
+    return r * (D / 2) + P::swz(r) * 16;
+  }
+  __device__ __forceinline__ static i32x2 column(const lds_u8* codes, int x, int at) {
+    return __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+        (__attribute__((address_space(3))) i32x2*)(codes + ((at ^ (x / 2 * 16)) + x % 2 * 8)));
+  }
+
+  // The weights of 64 keys as operands.
+  __device__ __forceinline__ static O operand(const f32x4* s) {
+    const float w[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
+    return pack_as<O, E>(w);
+  }
+
+  // Adds 64 weighted values to the output: the values as their codes times 2^(ref - 127), the weights (bf16, none negative)
+  // times 2^(e - ref), subtracted from their exponents down to 0. For scales e from ref - kSpan to ref; a weight beside a scale of
+  // 255 counts as 0.
+  __device__ __forceinline__ void values(const lds_u8* codes, const lds_u8* scales, int ref, int lane, const O (*p)[2]) {
+    const Scales sc = scales_of(scales, lane);
+    int at = rows_at(lane);
+    fresh_value(at);
+    const float power = __uint_as_float(uint32_t(ref) << 23);
+    const uint32_t top = uint32_t(ref << 7) * 0x10001u;
 #pragma unroll
     for (int b = 0; b < P::kP; ++b) {
-      float power[4][4];
+      const i32x2 c[2] = {column(codes, 2 * b, at), column(codes, 2 * b + 1, at)};
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int h = 0; h < 2; ++h) {
+        O f[kSets];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int byte = i * P::kP + b;
-          const uint32_t e = sc[j][byte / 4] >> (8 * (byte % 4)) & 255u;
-          power[j][i] = __uint_as_float(e << 23);
-          if (kOdd && e == 255u) power[j][i] = __uint_as_float(0x7FC00000u);
-        }
-      O p[kSets][2];
+        for (int w = 0; w < 4; ++w) {
+          // keys 2 (w % 2) and the next of subtile 2 h + w / 2
+          const int j = 2 * h + w / 2, one = w % 2 * 2 * P::kP + b, two = one + P::kP;
+          const u16x2 e = __builtin_bit_cast(u16x2, __builtin_amdgcn_perm(sc.w[j][two / 4], sc.w[j][one / 4],
+                                                                          0x0C000C00u | uint32_t(4 + two % 4) << 16 | uint32_t(one % 4)));
+          const u16x2 less = exponents_below(e, top);
 #pragma unroll
-      for (int z = 0; z < kSets; ++z)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float w[8];
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float x = s[z][2 * h + j][i];
-              w[4 * j + i] = kOdd && x == 0.0f ? 0.0f : x * power[2 * h + j][i];
-            }
-          p[z][h] = pack_as<O, E>(w);
+          for (int z = 0; z < kSets; ++z) lower(f[z], p[z][h], w, less);
         }
 #pragma unroll
-      for (int x = 2 * b; x < 2 * b + 2; ++x) {
-        const i32x2 w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(codes + r * (D / 2) + ((x / 2) ^ P::swz_v(r)) * 16 + x % 2 * 8));
+        for (int y = 0; y < 2; ++y) {
+          const u32x4 v = values_of(uint32_t(c[y][h]), power);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 v = values_of(uint32_t(w[h]), 1.0f);
-#pragma unroll
-          for (int z = 0; z < kSets; ++z) o[z][x] = mma16(v, p[z][h], o[z][x]);
+          for (int z = 0; z < kSets; ++z) o[z][2 * b + y] = mma16(v, f[z], o[z][2 * b + y]);
         }
       }
+      order();
     }
+  }
+
+  // Blocks of values that are NaN make the rows that see them (with a weight above 0) NaN in their columns.
+  __device__ __forceinline__ void mark(const lds_u8* scales, int lane, const O (*p)[2]) {
+#pragma unroll
+    for (int b = 0; b < P::kP; ++b)
+#pragma unroll
+      for (int z = 0; z < kSets; ++z) {
+        uint32_t hit = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t byte = scales[(16 * (i / 4) + 4 * (lane >> 4) + i % 4) * P::kP + b];
+          hit |= byte == 255u ? weight_bits(p[z][i / 8], i % 8) : 0u;
+        }
+        hit |= uint32_t(__shfl_xor(int(hit), 16));
+        hit |= uint32_t(__shfl_xor(int(hit), 32));
+        const float add = hit != 0 ? __uint_as_float(0x7FC00000u) : 0.0f;
+        o[z][2 * b] += add;
+        o[z][2 * b + 1] += add;
+        order();
+      }
   }
 };
 
@@ -354,24 +453,32 @@ __device__ __forceinline__ int32_t few_size(const AttnArgs& a, const Seq& s) {
   return x.hi - x.lo + kFewOver;
 }
 
+// The kernel's arguments, read anew: what only the start and the end of a unit use takes no scalar registers in between.
+__device__ __forceinline__ Attn4Args args_again() {
+  auto* p = (const __attribute__((address_space(4))) Attn4Args*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const Attn4Args*)p;
+}
+
 template <typename E, int D, int kSets>
-__global__ __launch_bounds__((Narrow4<E, D>::kThreads), (Narrow4<E, D>::kGroups)) void narrow4_kernel(Attn4Args a) {
-  using P = Narrow4<E, D>;
+__global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kSets>::kGroups)) void narrow4_kernel(Attn4Args a) {
+  using P = Narrow4<E, D, kSets>;
   using W = Wave4<E, D, kSets>;
-  __shared__ __align__(1024) unsigned char buf[P::kWaves * P::kBuffers * P::kTileBytes];
+  __shared__ __align__(1024) unsigned char buf[P::kWaves * P::kTileBytes];
+  __shared__ __align__(16) int32_t page_buf[P::kWaves * P::kRing * P::kSegs];
   __shared__ int64_t scan_part[P::kWaves];
-  __shared__ Seq found;
-  __shared__ int32_t found_seq;
-  __shared__ int64_t found_rest;
-  __shared__ float merge_c[P::kWaves][32], merge_l[P::kWaves][32];
+  __shared__ Seq found[P::kWaves];
+  __shared__ int32_t found_seq[P::kWaves];
+  __shared__ int64_t found_rest[P::kWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int b = blockIdx.x;
-  if (b == a.narrow.grid) {
+  const int b0 = blockIdx.x * P::kWaves, b = b0 + wave;   // this workgroup's first stretch, this wave's
+  if (b0 == a.narrow.grid) {
     list_row_tiles<Wide<E, D, uint16_t>, P::kThreads>(a, scan_part, a.sched, a.row_tiles, a.sched + 2 + a.max_tiles);
     return;
   }
 
-  // Total length, then the sequence that holds this stretch's start. Up to a sequence per thread both come of one scan.
+  // Total length, then the sequences that hold the starts of the waves' stretches. Up to a sequence per thread both come of
+  // one scan.
   Seq own = {0, 0, 0};
   int64_t total = 0, size = 0, upto = 0;
   for (int n0 = 0; n0 < a.N; n0 += P::kThreads) {
@@ -382,12 +489,9 @@ __global__ __launch_bounds__((Narrow4<E, D>::kThreads), (Narrow4<E, D>::kGroups)
     upto = block_scan<P::kThreads>(size, scan_part, sum);
     total += sum;
   }
-  if (tid == 0) a.narrow.joins[4 * b + 2] = 0;
   if (total == 0) return;
-  const Line line(total, a.narrow.grid, P::kWaves);
-  int64_t pos = line.start(b);
-  const int64_t end = line.start(b + 1);
-  if (pos >= end) return;
+  const Line line(total, a.narrow.grid, kFewOver + 1);
+  if (line.start(b0) >= total) return;
   int64_t found_before = 0;
   for (int n0 = 0;; n0 += P::kThreads) {
     int64_t sum = total;
@@ -397,195 +501,230 @@ __global__ __launch_bounds__((Narrow4<E, D>::kThreads), (Narrow4<E, D>::kGroups)
       size = int64_t(few_size(a, own)) * a.Hkv;
       upto = found_before + block_scan<P::kThreads>(size, scan_part, sum);
     }
-    if (pos >= upto - size && pos < upto) {
-      found = own;
-      found_seq = n0 + tid;
-      found_rest = pos - (upto - size);
+    for (int v = 0; v < P::kWaves; ++v) {
+      const int64_t at = line.start(b0 + v);
+      if (at >= upto - size && at < upto) {
+        found[v] = own;
+        found_seq[v] = n0 + tid;
+        found_rest[v] = at - (upto - size);
+      }
     }
     found_before += sum;
-    if (pos < found_before || n0 + P::kThreads >= a.N) break;
+    if (line.start(b0 + P::kWaves - 1) < found_before || n0 + P::kThreads >= a.N) break;
   }
   __syncthreads();
-  int n = __builtin_amdgcn_readfirstlane(found_seq);
-  int64_t rest = found_rest;   // position within the sequence's units
-  Seq s = {__builtin_amdgcn_readfirstlane(found.start), __builtin_amdgcn_readfirstlane(found.fresh),
-           __builtin_amdgcn_readfirstlane(found.kv)};
+  // From here on the waves go on by themselves.
+  int64_t pos = line.start(b);
+  const int64_t end = line.start(b + 1);
+  if (pos >= end) return;
+  int n = __builtin_amdgcn_readfirstlane(found_seq[wave]);
+  int64_t rest = uniform(found_rest[wave]);   // position within the sequence's units
+  Seq s = {__builtin_amdgcn_readfirstlane(found[wave].start), __builtin_amdgcn_readfirstlane(found[wave].fresh),
+           __builtin_amdgcn_readfirstlane(found[wave].kv)};
   W w;
-  lds_u8* const mine = (lds_u8*)buf + wave * P::kBuffers * P::kTileBytes;
+  lds_u8* const mine = (lds_u8*)buf + wave * P::kTileBytes;
   const uint32_t mine_at = uint32_t(uintptr_t(mine));
-  // what a lane loads: of codes, 16 bytes of row lane / kP of a load; of scales, 4 bytes of a key (two keys at D = 64)
-  const int code_row = lane / P::kP, code_col = lane % P::kP;
-  while (pos < end && n < a.N) {
-    const int32_t rows = int64_t(s.fresh) * a.group > kNarrowRows ? 0 : s.fresh * a.group;
+  lds_u8* const ring = (lds_u8*)page_buf + wave * P::kPageBytes;
+  const uint32_t ring_at = uint32_t(uintptr_t(ring));
+  // What a lane loads: of codes, 16 bytes of row lane / kP of a load; of scales, 4 bytes of a key (two keys at D = 64). Offsets
+  // from the place of the tile's first key in its page, and bytes from page to page. A load's first row and a lane's have no
+  // bit in common, so a page's mask and the swizzle apply to each.
+  const int mask = (1 << a.lps) - 1, code_row = lane / P::kP, scale_key = lane * 4 / P::kP;
+  const uint32_t code_page = uint32_t(a.Hkv << a.lps) * (D / 2), scale_page = uint32_t(a.Hkv << a.lps) * P::kP;
+  int code_lane = (code_row & mask) * (D / 2) + (lane % P::kP ^ P::swz(code_row)) * 16;
+  int scale_lane = (scale_key & mask) * P::kP + lane * 4 % P::kP;
+  const int seqs = a.N, lps = a.lps, window = a.window, last_of_cache = a.n_pages - 1;
+  const float scale2 = a.scale2;
+  while (pos < end && n < seqs) {
+    const Attn4Args before = args_again();
+    const int32_t rows = int64_t(s.fresh) * before.group > kNarrowRows ? 0 : s.fresh * before.group;
     if (rows == 0) {
-      if (++n < a.N) s = seq_of(a, n);
+      if (++n < seqs) s = seq_of(before, n);
       continue;
     }
-    const Span x = span_of<kFewKeys>(a, s, 0, rows - 1);
+    const Span x = span_of<kFewKeys>(before, s, 0, rows - 1);
     const int32_t tiles = x.hi - x.lo, size = tiles + kFewOver;
     const int hk = __builtin_amdgcn_readfirstlane(int(rest / size));
     const int32_t in = int32_t(rest - int64_t(hk) * size);   // where this stretch enters the unit and leaves it
     const int32_t out = int32_t(min(int64_t(size), in + (end - pos)));
     if (out <= kFewOver) break;   // left to the next workgroup
     const int32_t t0 = max(in - kFewOver, 0), t1 = out - kFewOver;
-    const_i32* row = (const_i32*)(a.table + int64_t(n) * a.width);
-    const int32_t last_page = max((s.kv - 1) >> a.lps, 0);
-    w.start(a, s, hk, rows, lane);
+    const int32_t* const row = before.table + int64_t(n) * before.width;
+    const int32_t last_page = max((s.kv - 1) >> lps, 0);
+    const typename W::Raw raw = w.queries(before, s, hk, rows, lane);
 
-    // the pages of the tile to load next are looked up one tile ahead: 8 rows lie in one page
-    constexpr int kSegs = kFewKeys / kSeg, kW = P::kWaves;
-    int32_t pages[kSegs];
-    int64_t at[kSegs];   // rows of the cache
+    // Asks for the pages of tile t, one for 8 keys.
     auto look_up = [&](int32_t t) {
-      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kFewKeys);
-#pragma unroll
-      for (int i = 0; i < kSegs; ++i) pages[i] = seg_page(a, row, last_page, kv0 + i * kSeg);
+      const int32_t j = (x.lo + t) * kFewKeys + lane * kSeg;
+      if (lane < P::kSegs)
+        load_lds4(ring_at + uint32_t((t - t0) % P::kRing * (P::kSegs * 4)),
+                  reinterpret_cast<const uint8_t*>(row + min(j >> lps, last_page)));
     };
+    // Where this lane's pieces of tile t lie, from the caches' starts.
+    uint64_t code_at[P::kCodeLoads], scale_at[P::kScaleLoads];
     auto locate = [&](int32_t t) {
-      const int32_t kv0 = __builtin_amdgcn_readfirstlane((x.lo + t) * kFewKeys);
-#pragma unroll
-      for (int i = 0; i < kSegs; ++i) at[i] = cache_row(a, pages[i], hk, kv0 + i * kSeg);
-    };
-    auto load = [&](const uint8_t* codes, const uint8_t* scales, uint32_t code_to, uint32_t scale_to, bool values) {
-      constexpr int kPer = P::kLoadRows / kSeg;   // segments of a load
+      const lds_u8* const pages = ring + (t - t0) % P::kRing * (P::kSegs * 4);
+      auto page = [&](int key) {
+        const int32_t p = *(const __attribute__((address_space(3))) int32_t*)(pages + key / kSeg * 4);
+        return uint32_t(min(max(p, 0), last_of_cache));
+      };
+      // the tile's place in its page, where one holds more than a tile
+      const uint32_t first = uint32_t(((hk << lps) + ((x.lo + t) * kFewKeys & mask)));
+      fresh_value(code_lane);
+      fresh_value(scale_lane);
 #pragma unroll
       for (int i = 0; i < P::kCodeLoads; ++i) {
-        const int r = i * P::kLoadRows + code_row;
-        const int64_t first = choose<kPer>(at + i * kPer, code_row / kSeg);
-        const int col = code_col ^ (values ? P::swz_v(r) : P::swz_k(r));
-        load_lds16(code_to + i * 1024, codes + first * (D / 2) + (code_row % kSeg) * (D / 2) + col * 16);
+        const int r = i * P::kLoadRows;
+        code_at[i] = uint64_t(page(r + code_row)) * code_page +
+                     ((first + (r & mask)) * uint32_t(D / 2) + uint32_t(code_lane ^ (P::swz(r) * 16)));
       }
 #pragma unroll
       for (int i = 0; i < P::kScaleLoads; ++i) {
-        const int byte = i * 256 + lane * 4, key = byte / P::kP;
-        constexpr int kOf = kSegs / P::kScaleLoads;
-        const int64_t first = choose<kOf>(at + i * kOf, key / kSeg % kOf);
-        if (byte < P::kScales) load_lds4(scale_to + i * 256, scales + first * P::kP + byte % (kSeg * P::kP));
+        const int key = i * 256 / P::kP;
+        scale_at[i] = uint64_t(page(key + scale_key % kFewKeys)) * scale_page + ((first + (key & mask)) * uint32_t(P::kP) + uint32_t(scale_lane));
       }
     };
-    auto load_keys = [&](uint32_t to) { load(a.kc, a.ks, to, to + 2 * P::kCodes, false); };
-    auto load_values = [&](uint32_t to) { load(a.vc, a.vs, to + P::kCodes, to + 2 * P::kCodes + P::kScaleBytes, true); };
-    look_up(t0 + wave);
-    wait_loads<0>();   // no store of the unit before is counted below
-    uint32_t half = 0;
+    auto load = [&](const uint8_t* codes, const uint8_t* scales, uint32_t code_to, uint32_t scale_to) {
+#pragma unroll
+      for (int i = 0; i < P::kCodeLoads; ++i) load_lds16(code_to + i * 1024, codes + code_at[i]);
+#pragma unroll
+      for (int i = 0; i < P::kScaleLoads; ++i)
+        if (i * 256 + lane * 4 < P::kScales) load_lds4(scale_to + i * 256, scales + scale_at[i]);
+    };
+    auto load_keys = [&]() {
+      const Attn4Args now = args_again();
+      load(now.kc, now.ks, mine_at, mine_at + 2 * P::kCodes);
+    };
+    auto load_values = [&]() {
+      const Attn4Args now = args_again();
+      load(now.vc, now.vs, mine_at + P::kCodes, mine_at + 2 * P::kCodes + P::kScaleBytes);
+    };
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i)
-      if (t0 + wave + i * kW < t1) {
-        locate(t0 + wave + i * kW);
-        load_keys(mine_at + i * P::kTileBytes);
-        load_values(mine_at + i * P::kTileBytes);
-        look_up(t0 + wave + (i + 1) * kW);
-      }
-    for (int32_t t = t0 + wave; t < t1; t += kW) {
-      const bool next = t + kW < t1, after = t + 2 * kW < t1;   // a further tile, and one for the buffer that this one leaves
+    for (int i = 0; i < P::kRing; ++i) look_up(t0 + i);
+    wait_loads<0>();   // the pages and the queries are there, and no store of the unit before is counted below
+    locate(t0);
+    load_keys();
+    load_values();
+    w.start(before, s, raw, rows, lane);
+    int ref = 0;
+    for (int32_t t = t0; t < t1; ++t) {
+      const bool next = t + 1 < t1;
       const int32_t kv0 = (x.lo + t) * kFewKeys;
-      const bool full = kv0 + kFewKeys - 1 <= x.first && (a.window == 0 || kv0 > x.last - a.window);
-      lds_u8* const tile = mine + half;
-      const lds_u8* const scales = tile + 2 * P::kCodes;
+      const bool full = kv0 + kFewKeys - 1 <= x.first && (window == 0 || kv0 > x.last - window);
+      const lds_u8* const scales = mine + 2 * P::kCodes;
       f32x4 sc[kSets][4];
-      // behind these keys are in flight: these values and the next tile
-      if (next) wait_loads<3 * P::kLoads>();
-      else wait_loads<P::kLoads>();
-      w.scores(tile, scales, lane, sc);
-      if (after) {
+      typename W::O p[kSets][2];
+      // Behind these keys these values are in flight; what the next tile is looked up with came before them.
+      wait_loads<P::kLoads>();
+      w.scores(mine, scales, lane, sc);
+      if (next) {
+        locate(t + 1);
         wait_reads();
-        locate(t + 2 * kW);
-        load_keys(mine_at + half);
+        look_up(t + P::kRing);
+        load_keys();
       }
 #pragma unroll
-      for (int z = 0; z < kSets; ++z) w.weights(a, z, sc[z], kv0, full, lane);
-      // behind these values: the keys just asked for and the next tile
-      if (after) wait_loads<3 * P::kLoads>();
-      else if (next) wait_loads<2 * P::kLoads>();
+      for (int z = 0; z < kSets; ++z) {
+        w.weights(scale2, z, sc[z], kv0, full, lane);
+        p[z][0] = W::operand(sc[z]);
+        p[z][1] = W::operand(sc[z] + 2);
+      }
+      // behind these values: the keys just asked for
+      if (next) wait_loads<P::kLoads>();
       else wait_loads<0>();
-      // whether a block among the values is NaN: a key's scales per lane
-      uint32_t nan = 0;
+      // a key's scales per lane; what lies behind the last key is not looked at
+      uint32_t own[(P::kP + 3) / 4];
 #pragma unroll
       for (int i = 0; i < (P::kP + 3) / 4; ++i) {
-        uint32_t z;
-        if constexpr (P::kP == 2) z = *(const __attribute__((address_space(3))) uint16_t*)(scales + P::kScaleBytes + lane * 2);
-        else z = *(const __attribute__((address_space(3))) uint32_t*)(scales + P::kScaleBytes + lane * P::kP + 4 * i);
-        nan |= ((z & 0x7F7F7F7Fu) + 0x01010101u) & z;
+        const lds_u8* const at = scales + P::kScaleBytes + lane * P::kP + 4 * i;
+        if constexpr (P::kP == 2) own[i] = *(const __attribute__((address_space(3))) uint16_t*)at * 0x10001u;
+        else own[i] = *(const __attribute__((address_space(3))) uint32_t*)at;
       }
-      if (__any((nan & 0x80808080u) != 0)) w.template values<true>(tile + P::kCodes, scales + P::kScaleBytes, lane, sc);
-      else w.template values<false>(tile + P::kCodes, scales + P::kScaleBytes, lane, sc);
-      if (after) {
+      const bool there = kv0 + lane < s.kv;
+      constexpr int kBytes = 4 * ((P::kP + 3) / 4);
+      auto byte = [&](int i) { return own[i / 4] >> (8 * (i % 4)) & 255u; };
+      auto largest = [&]() {   // of the bytes below 255
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kBytes; ++i) top = max(top, there && byte(i) < 255u ? byte(i) : 0u);
+        for (int d = 32; d > 0; d /= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
+        return int(__builtin_amdgcn_readfirstlane(top));
+      };
+      bool bands = __any(there && !within<P::kP>(own, ref));
+      if (bands) {
+        ref = largest();
+        bands = __any(there && !within<P::kP>(own, ref));
+        if (bands) w.mark(scales + P::kScaleBytes, lane, p);
+      }
+      for (;;) {
+        bool more = false;
+        if (bands) {
+          // scales too far apart, or NaN: a band of them at a time, 255 for the others
+          ref = largest();
+          uint32_t now[kBytes / 4] = {}, left = 0;
+#pragma unroll
+          for (int i = 0; i < kBytes; ++i) {
+            const bool in = int(byte(i)) <= ref && int(byte(i)) >= ref - kSpan;
+            now[i / 4] |= (in ? byte(i) : 255u) << (8 * (i % 4));
+            left |= uint32_t(!in && int(byte(i)) < ref);
+            if (in) own[i / 4] |= 255u << (8 * (i % 4));
+          }
+          more = __any(there && left);
+#pragma unroll
+          for (int i = 0; i < kBytes / 4; ++i) {
+            lds_u8* const at = mine + 2 * P::kCodes + P::kScaleBytes + lane * P::kP + 4 * i;
+            if constexpr (P::kP == 2) *(__attribute__((address_space(3))) uint16_t*)at = uint16_t(now[i]);
+            else *(__attribute__((address_space(3))) uint32_t*)at = now[i];
+          }
+          wait_reads();
+        }
+        w.values(mine + P::kCodes, scales + P::kScaleBytes, ref, lane, p);
+        if (!more) break;
+      }
+      if (next) {
         wait_reads();
-        load_values(mine_at + half);
-        look_up(t + 3 * kW);
+        load_values();
       }
-      half ^= P::kTileBytes;
     }
 
-    // The waves merge: maxima and sums first, then every thread sums some columns over the waves.
-    const int q = lane & 15, g = lane >> 4;
-    __syncthreads();   // the buffers are free
-    float* const sums = reinterpret_cast<float*>(buf);
+    // Rows of a unit that lies in this stretch are finished here; those of a piece go to the join.
+    const Attn4Args after = args_again();
+    const int g = lane >> 4;
+    const bool whole = t0 == 0 && t1 == tiles;
+    float* const part = after.narrow.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
 #pragma unroll
     for (int z = 0; z < kSets; ++z) {
-      const float l_all = quarter_sum(w.l[z]);
-      if (l_all != l_all && w.c[z] == -INFINITY) w.c[z] = 0.0f;   // all scores NaN: not a row that sees nothing
-      if (g == 0) {
-        merge_c[wave][z * 16 + q] = w.c[z];
-        merge_l[wave][z * 16 + q] = l_all;
-      }
-    }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == tiles;
-    float* const part = a.narrow.parts + int64_t(2 * b + (t0 == 0 ? 1 : 0)) * part_floats<D>(kNarrowRows);
-    // half of the columns at a time, in the buffers of the tiles
+      const int r = z * 16 + (lane & 15);
+      const float l = quarter_sum(w.l[z]);
+      if (l != l && w.c[z] == -INFINITY) w.c[z] = 0.0f;   // all scores NaN: not a row that sees nothing
+      if (r >= rows) continue;
+      if (whole) {
+        const bool none = w.c[z] == -INFINITY;
+        const float inv = none ? 0.0f : 1.0f / l;
+        const int64_t to = out_row(after, s, hk, r);
 #pragma unroll
-    for (int x0 = 0; x0 < D; x0 += D / 2) {
-      constexpr int kC = D / 2, kRow = kC + 4;   // 4 floats against bank conflicts
-      static_assert(P::kWaves * 32 * kRow * 4 <= int(sizeof(buf)), "merge buffer");
-#pragma unroll
-      for (int z = 0; z < kSets; ++z)
-        if (z * 16 + q < rows) {
-#pragma unroll
-          for (int y = 0; y < kC / 16; ++y)
-            *reinterpret_cast<f32x4*>(sums + (wave * 32 + z * 16 + q) * kRow + y * 16 + 4 * g) = w.o[z][x0 / 16 + y];
+        for (int y = 0; y < D / 16; ++y) {
+          const f32x4 v = none ? f32x4{0, 0, 0, 0} : w.o[z][y] * inv;
+          store4<E>(after.o + (to * D + y * 16 + 4 * g) * sizeof(E), v[0], v[1], v[2], v[3]);
         }
-      __syncthreads();
-      for (int e = tid; e < rows * (kC / 4); e += P::kThreads) {
-        const int qq = e / (kC / 4), d = (e % (kC / 4)) * 4;
-        float top = -INFINITY;
-        for (int v = 0; v < P::kWaves; ++v) top = fmaxf(top, merge_c[v][qq]);
-        const float base = top == -INFINITY ? 0.0f : top;
-        f32x4 acc = 0.0f;
-        float l = 0.0f;
-        for (int v = 0; v < P::kWaves; ++v) {
-          // a part without weights counts too, by a factor of 0: what it saw may have been NaN
-          const float f = __builtin_amdgcn_exp2f(merge_c[v][qq] - base);
-          acc += f * *reinterpret_cast<const f32x4*>(sums + (v * 32 + qq) * kRow + d);
-          l += f * merge_l[v][qq];
-        }
-        const int col = x0 + d;
-        if (whole) {
-          const float inv = top == -INFINITY ? 0.0f : 1.0f / l;
-          if (top == -INFINITY) acc = 0.0f;
-          const int64_t r = out_row(a, s, hk, qq);
-          store4<E>(a.o + (r * D + col) * sizeof(E), acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
-          if (a.lse != nullptr && col == 0) a.lse[r] = top == -INFINITY ? -INFINITY : (top + log2f(l)) * kLn2;
-        } else {
-          *reinterpret_cast<f32x4*>(part + qq * D + col) = acc;
-          if (col == 0) {
-            part[kNarrowRows * D + qq] = top;
-            part[kNarrowRows * (D + 1) + qq] = l;
-          }
+        if (after.lse != nullptr && g == 0) after.lse[to] = none ? -INFINITY : (w.c[z] + log2f(l)) * kLn2;
+      } else {
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) *reinterpret_cast<f32x4*>(part + r * D + y * 16 + 4 * g) = w.o[z][y];
+        if (g == 0) {
+          part[kNarrowRows * D + r] = w.c[z];
+          part[kNarrowRows * (D + 1) + r] = l;
         }
       }
-      __syncthreads();
     }
-    if (tid == 0 && t0 > 0 && line.start(b - 1) <= pos - in + kFewOver) {
-      // the first cut of this unit: the one before is not within it
-      a.narrow.joins[4 * b] = n;
-      a.narrow.joins[4 * b + 1] = hk;
-      a.narrow.joins[4 * b + 3] = 0;
-      a.narrow.joins[4 * b + 2] = int32_t(1 + line.before(pos - in + size) - b);
+    if (lane == 0 && t0 == 0) {   // the unit's first piece
+      int32_t* const join = after.narrow.joins + 2 * (int64_t(n) * after.Hkv + hk);
+      join[0] = whole ? 0 : int32_t(line.before(pos - in + size) - b);
+      join[1] = b + 1;
     }
     pos += out - in;
-    rest = out < size ? rest + (out - in) : (hk + 1 < a.Hkv ? int64_t(hk + 1) * size : 0);
-    if (out == size && hk + 1 == a.Hkv && ++n < a.N) s = seq_of(a, n);
+    rest = out < size ? rest + (out - in) : (hk + 1 < after.Hkv ? int64_t(hk + 1) * size : 0);
+    if (out == size && hk + 1 == after.Hkv && ++n < seqs) s = seq_of(after, n);
   }
 }
 
@@ -595,12 +734,22 @@ constexpr int kFewUnits4 = 64;
 
 template <typename E, int D>
 Plan plan4_of(const rglru_paged_shape_t& s) {
-  return plan_of<Narrow4<E, D>, Wide<E, D, uint16_t>, D>(s, kFewKeys, kFewUnits4);
+  using W = Wide<E, D, uint16_t>;
+  return most_rows(s) <= 16 ? plan_of<Narrow4<E, D, 1>, W, D>(s, kFewKeys, kFewUnits4)
+                            : plan_of<Narrow4<E, D, 2>, W, D>(s, kFewKeys, kFewUnits4);
 }
 
 template <typename E, int D>
 size_t bytes_of(const rglru_paged_shape_t& s) {
-  return plan4_of<E, D>(s).bytes;
+  // a call of fewer tokens than the workspace was made for may take one set of rows, and more workgroups
+  const size_t one = plan_of<Narrow4<E, D, 1>, Wide<E, D, uint16_t>, D>(s, kFewKeys, kFewUnits4).bytes, now = plan4_of<E, D>(s).bytes;
+  return now > one ? now : one;
+}
+
+template <typename E, int D, int kSets>
+void launch_narrow(const Attn4Args& a, const Plan& p, hipStream_t st) {
+  using P = Narrow4<E, D, kSets>;
+  narrow4_kernel<E, D, kSets><<<unsigned(p.narrow_grid / P::kStretches + p.wide), P::kThreads, 0, st>>>(a);
 }
 
 template <typename E, int D>
@@ -608,16 +757,12 @@ void launch(const rglru_paged_shape_t& s, Attn4Args a, uint8_t* workspace, hipSt
   using W = Wide<E, D, uint16_t>;
   const Plan p = plan4_of<E, D>(s);
   lay_out(a, p, workspace);
-  if (p.narrow) {
-    const unsigned grid = unsigned(p.narrow_grid + p.wide);
-    if (most_rows(s) <= 16) narrow4_kernel<E, D, 1><<<grid, Narrow4<E, D>::kThreads, 0, st>>>(a);
-    else narrow4_kernel<E, D, 2><<<grid, Narrow4<E, D>::kThreads, 0, st>>>(a);
-  }
+  if (p.narrow) most_rows(s) <= 16 ? launch_narrow<E, D, 1>(a, p, st) : launch_narrow<E, D, 2>(a, p, st);
   if (p.wide) {
     if (!p.narrow && !p.own_list) sched_kernel<W><<<1, kSchedThreads, 0, st>>>(a);
     wide_kernel<E, D, Staged<E, D>><<<unsigned(p.wide_grid), W::kThreads, 0, st>>>(a);
   }
-  join<E, D, W>(s, a, p, st);
+  join<E, D, W, true>(s, a, p, st);
 }
 
 }  // namespace
