@@ -30,7 +30,8 @@ __device__ __forceinline__ int32_t wave_inclusive(int32_t v, int lane) {
   return v;
 }
 
-// The same over the threads of a workgroup; `total` is the sum of all. `part`: kWaves words of LDS.
+// The same over the threads of a workgroup; `total` is the sum of all. `part`: a word of LDS for every wave.
+template <int kAll = kThreads>
 __device__ __forceinline__ int32_t block_inclusive(int32_t v, int32_t* part, int32_t& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   v = wave_inclusive(v, lane);
@@ -38,7 +39,7 @@ __device__ __forceinline__ int32_t block_inclusive(int32_t v, int32_t* part, int
   if (lane == 63) part[wave] = v;
   __syncthreads();
   total = 0;
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < kAll / 64; ++w) {
     if (w < wave) v += part[w];
     total += part[w];
   }
@@ -49,6 +50,15 @@ __device__ __forceinline__ int32_t block_sum(int32_t v, int32_t* part) {
   int32_t total;
   block_inclusive(v, part, total);
   return total;
+}
+
+// A bit for every page, in LDS: pools of up to kSmallPages pages.
+constexpr int kSmallThreads = 1024, kSmallPages = 1 << 17, kSmallWords = kSmallPages / 32;
+
+// The pages of a word from `first` on.
+__device__ __forceinline__ uint32_t bits_from(int word, int32_t first) {
+  const int32_t p0 = word * 32;
+  return first <= p0 ? ~0u : first >= p0 + 32 ? 0u : ~0u << (first - p0);
 }
 
 struct Rows {
@@ -228,9 +238,100 @@ __global__ __launch_bounds__(kThreads) void free_list_kernel(FreeArgs a) {
   if (blockIdx.x == 0 && tid == 0) a.count_out[0] = min(base + total, a.r.n_pages);
 }
 
+// Small pools: one workgroup, one launch, a bit in LDS for a page that is freed. The entries that rows give up stand in one
+// line, so that every thread has a few to look up beside each other. The first to give a page up marks it, further ones take
+// its count down; then every marked page either goes onto the list, its place from the sums over the marks, or has its count
+// taken down for the first one. A CU's atomics are slow (8 000 pages given up, 28 000 in the pool: 20 us with two on memory for each, 15 so).
+constexpr int kSmallFree = 1 << 14, kSmallCompact = 1 << 15, kSmallRows = 2048;   // entries of the table, rows
+
+__global__ __launch_bounds__(kSmallThreads) void free_small_kernel(FreeArgs a) {
+  __shared__ uint32_t gone[kSmallWords];
+  __shared__ int32_t before[kSmallWords];
+  __shared__ int32_t stays[kSmallRows], ends[kSmallRows];   // a row's first entry given up; entries of the rows up to it
+  __shared__ int32_t part[kSmallThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, words = (a.r.n_pages + 31) / 32, padded = (a.r.n_pages + 63) / 64 * 64;
+  for (int w = tid; w < padded / 32; w += kSmallThreads) gone[w] = 0;
+  int32_t all = 0;
+  for (int n0 = 0; n0 < a.r.N; n0 += kSmallThreads) {
+    const int n = n0 + tid;
+    int32_t given = 0, total;
+    if (n < a.r.N) {
+      const int32_t held = a.held[n], kept = min(max(a.keep[n], 0), held);
+      a.held_out[n] = kept;
+      stays[n] = pages_of(a.r, kept);
+      given = max(pages_of(a.r, held) - stays[n], 0);
+    }
+    const int32_t upto = block_inclusive<kSmallThreads>(given, part, total);
+    if (n < a.r.N) ends[n] = all + upto;
+    all += total;
+  }
+  __syncthreads();
+  constexpr int kAhead = 4;
+  for (int i0 = tid; i0 < all; i0 += kAhead * kSmallThreads) {
+    int32_t page[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = min(i0 + k * kSmallThreads, all - 1);
+      int lo = 0, hi = a.r.N - 1;   // the first row that ends behind i
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (ends[mid] > i) hi = mid; else lo = mid + 1;
+      }
+      page[k] = a.r.table[int64_t(lo) * a.r.width + stays[lo] + i - (lo > 0 ? ends[lo - 1] : 0)];
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kSmallThreads < all && page[k] >= 0 && page[k] < a.r.n_pages) {
+        const uint32_t bit = 1u << (page[k] % 32);
+        if (atomicOr(gone + page[k] / 32, bit) & bit) atomicSub(a.shares + page[k], 1);
+      }
+  }
+  __threadfence();
+  __syncthreads();
+  for (int p0 = tid; p0 < padded; p0 += kAhead * kSmallThreads) {
+    int32_t shares[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + k * kSmallThreads;
+      shares[k] = p < a.r.n_pages && (gone[p / 32] >> (p % 32) & 1) ? a.shares[p] : INT32_MAX;
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int p = p0 + k * kSmallThreads;
+      if (p >= padded) break;
+      const bool marked = p < a.r.n_pages && (gone[p / 32] >> (p % 32) & 1);
+      const uint64_t free = __ballot(marked && shares[k] <= 0);
+      if (marked && shares[k] != 0) a.shares[p] = max(shares[k] - 1, 0);
+      if (lane == 0) gone[p / 32] = uint32_t(free), gone[p / 32 + 1] = uint32_t(free >> 32);
+    }
+  }
+  __syncthreads();
+  const int each = (words + kSmallThreads - 1) / kSmallThreads, first = tid * each, end = min(first + each, words);
+  int32_t mine = 0, total;
+  for (int w = first; w < end; ++w) mine += __popc(gone[w]);
+  int32_t upto = block_inclusive<kSmallThreads>(mine, part, total) - mine;
+  for (int w = first; w < end; ++w) {
+    before[w] = upto;
+    upto += __popc(gone[w]);
+  }
+  __syncthreads();
+  const int32_t count = min(max(a.count[0], 0), a.r.n_pages);
+  for (int p = tid; p < a.r.n_pages; p += kSmallThreads) {
+    const uint32_t word = gone[p / 32];
+    if (!(word >> (p % 32) & 1)) continue;
+    const int32_t at = count + total - 1 - (before[p / 32] + __popc(word & ((1u << (p % 32)) - 1)));
+    if (at < a.r.n_pages) a.free_pages[at] = p;
+  }
+  if (tid == 0) a.count_out[0] = min(count + total, a.r.n_pages);
+}
+
 // ---- compact ----
 //
-// Five launches: marks to 0; marks of the pages that rows hold and of those
+// Small pools: one launch. Every workgroup marks the pages in use and the free
+// ones for itself, in LDS, with the sums before every 32 of them, and writes
+// its share of the outputs; where the i-th page moves to is looked up in the sums.
+//
+// Others, five launches: marks to 0; marks of the pages that rows hold and of those
 // on the free list; counts per chunk; ranks, which give the pairs and the new
 // list; and the table and the counts of sharing, which follow the ranks.
 struct CompactArgs {
@@ -368,6 +469,100 @@ __global__ __launch_bounds__(kThreads) void compact_apply_kernel(CompactArgs a) 
   }
 }
 
+// Page number `rank` among the set bits: the word by its sum, then the bit.
+__device__ __forceinline__ int32_t select(const uint32_t* bits, const int32_t* before, int words, int32_t rank) {
+  int lo = 0, hi = words - 1;   // the last word whose sum is at most rank
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (before[mid] <= rank) lo = mid; else hi = mid - 1;
+  }
+  uint32_t left = bits[lo];
+  for (int32_t skip = rank - before[lo]; skip > 0; --skip) left &= left - 1;
+  return lo * 32 + __ffs(left) - 1;
+}
+
+__global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArgs a) {
+  __shared__ uint32_t go[kSmallWords], to[kSmallWords];   // pages to move, places
+  __shared__ int32_t go_before[kSmallWords], to_before[kSmallWords];
+  __shared__ int32_t part[kSmallThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, words = (a.r.n_pages + 31) / 32;
+  for (int w = tid; w < words; w += kSmallThreads) go[w] = to[w] = 0;
+  __syncthreads();
+  const int32_t listed = min(max(a.count[0], 0), a.r.n_pages);
+  for (int i = tid; i < listed; i += kSmallThreads) {
+    const int32_t p = a.free_pages[i];
+    if (p >= 0 && p < a.r.n_pages) atomicOr(to + p / 32, 1u << (p % 32));
+  }
+  for (int n = wave; n < a.r.N; n += kSmallThreads / 64) {
+    const int32_t have = pages_of(a.r, a.held[n]);
+    const int32_t* const row = a.r.table + int64_t(n) * a.r.width;
+    for (int32_t j = lane; j < have; j += 64) {
+      const int32_t p = row[j];
+      if (p >= 0 && p < a.r.n_pages) atomicOr(go + p / 32, 1u << (p % 32));
+    }
+  }
+  __syncthreads();
+  const int each = (words + kSmallThreads - 1) / kSmallThreads, first = tid * each, end = min(first + each, words);
+  int32_t go_mine = 0, to_mine = 0, go_all, to_all;
+  for (int w = first; w < end; ++w) {
+    const uint32_t behind = bits_from(w, a.keep), used = go[w];
+    to[w] &= ~used & ~behind;
+    go[w] = used & behind;
+    go_mine += __popc(go[w]);
+    to_mine += __popc(to[w]);
+  }
+  int32_t go_at = block_inclusive<kSmallThreads>(go_mine, part, go_all) - go_mine;
+  int32_t to_at = block_inclusive<kSmallThreads>(to_mine, part, to_all) - to_mine;
+  for (int w = first; w < end; ++w) {
+    go_before[w] = go_at;
+    to_before[w] = to_at;
+    go_at += __popc(go[w]);
+    to_at += __popc(to[w]);
+  }
+  __syncthreads();
+  const int32_t moves = min(go_all, to_all), left = to_all - moves;
+  const int threads = gridDim.x * kSmallThreads, start = blockIdx.x * kSmallThreads + tid;
+  auto rank_of = [](const uint32_t* bits, const int32_t* before, int32_t p) {
+    return before[p / 32] + __popc(bits[p / 32] & ((1u << (p % 32)) - 1));
+  };
+  auto marked = [](const uint32_t* bits, int32_t p) { return bits[p / 32] >> (p % 32) & 1; };
+  for (int i = start; i < a.r.N * a.r.width; i += threads) {
+    const int n = i / a.r.width;
+    int32_t p = a.r.table[i];
+    if (p >= a.keep && p < a.r.n_pages && i - n * a.r.width < pages_of(a.r, a.held[n])) {   // so it is marked
+      const int32_t rank = rank_of(go, go_before, p);
+      if (rank < moves) p = select(to, to_before, words, rank);
+    }
+    a.table_out[i] = p;
+  }
+  for (int32_t p = start; p < a.r.n_pages; p += threads) {
+    int32_t shares = a.shares[p];
+    if (marked(go, p)) {
+      const int32_t rank = rank_of(go, go_before, p);
+      if (rank < moves) {
+        a.pairs[2 * rank] = p;
+        shares = 0;
+      }
+    } else if (marked(to, p)) {
+      const int32_t rank = rank_of(to, to_before, p);
+      if (rank < moves) {
+        a.pairs[2 * rank + 1] = p;
+        shares = a.shares[select(go, go_before, words, rank)];
+      } else {
+        a.free_out[to_all - 1 - rank] = p;
+      }
+    }
+    a.shares_out[p] = shares;
+    if (p >= left) a.free_out[p] = -1;
+    if (p >= moves && p < a.most) a.pairs[2 * p] = a.pairs[2 * p + 1] = -1;
+  }
+  if (start == 0) {
+    a.count_out[0] = left;
+    a.n_pairs[0] = moves;
+    a.unmoved[0] = go_all - moves;
+  }
+}
+
 // ---- copy ----
 //
 // Bound by HBM: a workgroup copies pieces of up to kPieceBytes of one page of one
@@ -432,6 +627,12 @@ int64_t most(int64_t a, int64_t b) { return a > b ? a : b; }
 dim3 row_grid(const rglru_paged_shape_t& s) {
   const int64_t x = least(ceil_div(s.n_seqs, kWaves), 1024);
   return dim3(unsigned(x), unsigned(least(ceil_div(s.max_pages, kSlice), most(2048 / x, 1))));
+}
+
+// Pools that one launch takes. us on the GPU, one launch and several: free, 8 000 entries of the table 10.4 and 9.0, 16 000 11.7
+// and 10.0, 32 000 15 and 11; compact 9.3 and 14.4, 11.1 and 15.2, 15 to 17 and 15 to 16. On the host every launch costs 2.6.
+bool small(const rglru_paged_shape_t& s, int entries) {
+  return s.n_pages <= kSmallPages && s.n_seqs <= kSmallRows && int64_t(s.n_seqs) * s.max_pages <= entries;
 }
 
 size_t free_bytes(const rglru_paged_shape_t& s) { return round_up(size_t(ceil_div(s.n_pages, kChunk)) * 4, 16); }
@@ -523,6 +724,10 @@ extern "C" rglru_status_t rglru_page_free(const rglru_paged_shape_t* sp, const i
   a.counts = static_cast<int32_t*>(workspace);
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (paged::small(s, paged::kSmallFree)) {
+    paged::free_small_kernel<<<1, paged::kSmallThreads, 0, st>>>(a);
+    return launch_status();
+  }
   paged::free_mark_kernel<<<paged::row_grid(s), paged::kThreads, 0, st>>>(a);
   paged::free_count_kernel<<<unsigned(a.chunks), paged::kThreads, 0, st>>>(a);
   paged::free_list_kernel<<<unsigned(a.chunks), paged::kThreads, 0, st>>>(a);
@@ -576,6 +781,11 @@ extern "C" rglru_status_t rglru_page_compact(const rglru_paged_shape_t* sp, int6
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   a.most = int32_t(room);
   const hipStream_t st = static_cast<hipStream_t>(stream);
+  if (paged::small(s, paged::kSmallCompact)) {
+    const int64_t all = paged::most(int64_t(s.n_seqs) * s.max_pages, s.n_pages);
+    paged::compact_small_kernel<<<unsigned(ceil_div(all, paged::kSmallThreads)), paged::kSmallThreads, 0, st>>>(a);
+    return launch_status();
+  }
   const int64_t words = int64_t(space.counts) / 16;
   paged::compact_clear_kernel<<<unsigned(ceil_div(words, paged::kThreads)), paged::kThreads, 0, st>>>(
       reinterpret_cast<paged::u32x4*>(at), words);

@@ -820,20 +820,31 @@ def rglru_paged_attn_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return o, lse
 
 
-def _q4_cache(k_codes, k_scales, v_codes, v_scales, device):
-    """Checks the four arrays of a 4-bit cache; returns its shape [n_pages, Hkv, page_size, D]."""
-    if not isinstance(k_codes, torch.Tensor) or k_codes.dim() != 4:
+@functools.lru_cache(maxsize=256)
+def _q4_rows(shape):
+    """(n_pages, Hkv, page_size, D) of codes [n_pages, Hkv, page_size, D / 2], and the shape of their scales."""
+    if len(shape) != 4:
         raise ValueError("k_codes must be a tensor [n_pages, Hkv, page_size, D / 2]")
-    rows, dim = tuple(k_codes.shape[:3]), 2 * k_codes.shape[3]
-    if dim % 32 != 0:
-        raise ValueError(f"k_codes has rows of {dim // 2} bytes, expected a multiple of 16 (blocks of 32 elements)")
-    if max(rows[1], rows[2], dim) >> 31:
-        raise ValueError(f"k_codes has shape {tuple(k_codes.shape)}, expected heads, page size and width below 2^31")
-    _need(k_codes, "k_codes", (*rows, dim // 2), torch.uint8, device)
-    _need(v_codes, "v_codes", (*rows, dim // 2), torch.uint8, device)
-    _need(k_scales, "k_scales", (*rows, dim // 32), torch.uint8, device)
-    _need(v_scales, "v_scales", (*rows, dim // 32), torch.uint8, device)
-    return (*rows, dim)
+    n_pages, heads, page_size, half = shape
+    if half % 16 != 0:
+        raise ValueError(f"k_codes has rows of {half} bytes, expected a multiple of 16 (blocks of 32 elements)")
+    if max(heads, page_size, 2 * half) >> 31:
+        raise ValueError(f"k_codes has shape {tuple(shape)}, expected heads, page size and width below 2^31")
+    return n_pages, heads, page_size, 2 * half, torch.Size((n_pages, heads, page_size, half // 16))
+
+
+def _q4_cache(k_codes, k_scales, v_codes, v_scales):
+    """Checks the four arrays of a 4-bit cache; returns its device and shape (n_pages, Hkv, page_size, D)."""
+    if not isinstance(k_codes, torch.Tensor):
+        raise TypeError("k_codes must be a tensor")
+    device, shape = k_codes.device, k_codes.shape
+    n_pages, heads, page_size, dim, scales = _q4_rows(shape)
+    u8 = torch.uint8
+    _need(k_codes, "k_codes", shape, u8, device)
+    _need(v_codes, "v_codes", shape, u8, device)
+    _need(k_scales, "k_scales", scales, u8, device)
+    _need(v_scales, "v_scales", scales, u8, device)
+    return device, n_pages, heads, page_size, dim
 
 
 def rglru_paged_kv_write_q4(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Tensor, k_scales: torch.Tensor,
@@ -846,10 +857,7 @@ def rglru_paged_kv_write_q4(k: torch.Tensor, v: torch.Tensor, k_codes: torch.Ten
     code. A block with an infinity or NaN reads as NaN. k and v: float32 or bfloat16, possibly slices of wider rows
     (one stride for both)."""
     lib = _lib.load()
-    if not isinstance(k_codes, torch.Tensor):
-        raise TypeError("k_codes must be a tensor")
-    dev = k_codes.device
-    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    dev, n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales)
     if not isinstance(k, torch.Tensor) or k.dtype not in _IO:
         raise ValueError("k must be a float32 or bfloat16 tensor")
     t, row = _rows(k, "k", heads, dim, k.dtype, dev)
@@ -869,17 +877,17 @@ def rglru_paged_kv_read_q4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_code
 
     Returns (k, v), [T, Hkv, D] of `dtype` (float32 or bfloat16)."""
     lib = _lib.load()
-    if not isinstance(k_codes, torch.Tensor):
-        raise TypeError("k_codes must be a tensor")
-    dev = k_codes.device
-    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    dev, n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales)
     if dtype not in _IO:
         raise ValueError(f"unsupported dtype {dtype}")
     if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
         raise ValueError("slot_map must be a tensor [T]")
     t = slot_map.numel()
     _need(slot_map, "slot_map", (t,), torch.int32, dev)
-    k, v = (_out(x, name, (t, heads, dim), dtype, dev) for x, name in ((k, "k"), (v, "v")))
+    if k is None and v is None:
+        k, v = torch.empty((2, t, heads, dim), dtype=dtype, device=dev).unbind()
+    else:
+        k, v = _out(k, "k", (t, heads, dim), dtype, dev), _out(v, "v", (t, heads, dim), dtype, dev)
     shape = _paged_shape(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[dtype], 0, 0, 0.0, 0, 0)
     _call_on(dev, lib.rglru_paged_kv_read_q4, "rglru_paged_kv_read_q4", ctypes.byref(shape), k_codes.data_ptr(),
              k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr())
@@ -906,10 +914,7 @@ def rglru_paged_attn_q4_fwd(q: torch.Tensor, k_codes: torch.Tensor, k_scales: to
     rglru_paged_attn_q4_workspace_bytes bytes, as there. Returns (o [T, Hq, D], lse [T, Hq] float32 or None); padding
     rows are left as they were."""
     lib = _lib.load()
-    if not isinstance(k_codes, torch.Tensor):
-        raise TypeError("k_codes must be a tensor")
-    dev = k_codes.device
-    n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales, dev)
+    dev, n_pages, heads, page_size, dim = _q4_cache(k_codes, k_scales, v_codes, v_scales)
     if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.dtype not in _IO:
         raise ValueError("q must be a float32 or bfloat16 tensor [T, Hq, D]")
     hq = _int32("Hq", q.shape[1])
@@ -935,26 +940,26 @@ def rglru_paged_attn_q4_fwd(q: torch.Tensor, k_codes: torch.Tensor, k_scales: to
 
 
 def _pool(block_table, lens, name, shares, free_pages, free_count, page_size):
-    """Checks the arrays of a page pool; returns its shape and device."""
+    """Checks the arrays of a page pool; returns its shape, device, rows and pages."""
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a tensor [N, max_pages]")
-    dev = block_table.device
-    n = _int32("the number of rows", block_table.shape[0])
-    width = _table(block_table, n, dev)
-    _need(lens, name, (n,), torch.int32, dev)
+    dev, i32 = block_table.device, torch.int32
+    n, width = block_table.shape
+    if (n | width) >> 31:
+        raise ValueError(f"block_table has shape {(n, width)}, expected less than 2^31 rows and columns")
+    _need(block_table, "block_table", (n, width), i32, dev)
+    _need(lens, name, (n,), i32, dev)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be a tensor [n_pages]")
-    n_pages = free_pages.numel()
-    _need(free_pages, "free_pages", (n_pages,), torch.int32, dev)
-    _need(shares, "shares", (n_pages,), torch.int32, dev)
-    _need(free_count, "free_count", (1,), torch.int32, dev)
-    return _paged_shape(0, n_pages, n, width, _int32("page_size", page_size), 0, 0, 0, 0, 0, 0, 0.0, 0, 0), dev
+    n_pages = free_pages.shape[0]
+    _need(free_pages, "free_pages", (n_pages,), i32, dev)
+    _need(shares, "shares", (n_pages,), i32, dev)
+    _need(free_count, "free_count", (1,), i32, dev)
+    return _paged_shape(0, n_pages, n, width, _int32("page_size", page_size), 0, 0, 0, 0, 0, 0, 0.0, 0, 0), dev, n, n_pages
 
 
-def _pool_outs(outs, names, sizes, device):
-    if outs.count(None) == len(outs):   # pieces of one allocation
-        return torch.empty(sum(sizes), dtype=torch.int32, device=device).split_with_sizes(sizes)
-    return tuple(_out(o, k, (m,), torch.int32, device) for o, k, m in zip(outs, names, sizes))
+def _given(outs):
+    return any(o is not None for o in outs)
 
 
 def _pool_scratch(workspace, nbytes, device):
@@ -962,6 +967,13 @@ def _pool_scratch(workspace, nbytes, device):
         return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
     _scratch(workspace, device)
     return workspace
+
+
+@functools.lru_cache(maxsize=256)
+def _pool_bytes(which, n_pages, n, width, page_size):
+    """The workspace of rglru_page_free or rglru_page_compact, in bytes (a multiple of 16)."""
+    shape = _paged_shape(0, n_pages, n, width, page_size, 0, 0, 0, 0, 0, 0, 0.0, 0, 0)
+    return int(getattr(_lib.load(), which)(ctypes.byref(shape)))
 
 
 def rglru_page_fork(fork_from: torch.Tensor, lens: torch.Tensor, block_table: torch.Tensor, shares: torch.Tensor,
@@ -978,19 +990,18 @@ def rglru_page_fork(fork_from: torch.Tensor, lens: torch.Tensor, block_table: to
     not empty, or for which no page is left is not served and stays as it was.
     Returns (pairs [N, 2]: from, to or -1, -1; lens_out [N]; held_lens_out [N]; free_count_out [1]; unserved [1])."""
     lib = _lib.load()
-    shape, dev = _pool(block_table, lens, "lens", shares, free_pages, free_count, page_size)
-    n = shape.n_seqs
-    _need(fork_from, "fork_from", (n,), torch.int32, dev)
-    _opt(held_lens, "held_lens", (n,), torch.int32, dev)
-    names = ("lens_out", "held_lens_out", "free_count_out", "unserved")
-    if pairs is None and lens_out is None and held_lens_out is None and free_count_out is None and unserved is None:
-        pairs, lens_out, held_lens_out, free_count_out, unserved = torch.empty(
-            4 * n + 2, dtype=torch.int32, device=dev).split_with_sizes((2 * n, n, n, 1, 1))
+    shape, dev, n, _ = _pool(block_table, lens, "lens", shares, free_pages, free_count, page_size)
+    i32 = torch.int32
+    _need(fork_from, "fork_from", (n,), i32, dev)
+    _opt(held_lens, "held_lens", (n,), i32, dev)
+    if _given((pairs, lens_out, held_lens_out, free_count_out, unserved)):
+        pairs = _out(pairs, "pairs", (n, 2), i32, dev)
+        lens_out, held_lens_out = _out(lens_out, "lens_out", (n,), i32, dev), _out(held_lens_out, "held_lens_out", (n,), i32, dev)
+        free_count_out, unserved = _out(free_count_out, "free_count_out", (1,), i32, dev), _out(unserved, "unserved", (1,), i32, dev)
+    else:   # pieces of one allocation
+        pairs, lens_out, held_lens_out, free_count_out, unserved = torch.empty(4 * n + 2, dtype=i32, device=dev).split_with_sizes(
+            (2 * n, n, n, 1, 1))
         pairs = pairs.view(n, 2)
-    else:
-        pairs = _out(pairs, "pairs", (n, 2), torch.int32, dev)
-        lens_out, held_lens_out, free_count_out, unserved = _pool_outs(
-            (lens_out, held_lens_out, free_count_out, unserved), names, (n, n, 1, 1), dev)
     _call_on(dev, lib.rglru_page_fork, "rglru_page_fork", ctypes.byref(shape), fork_from.data_ptr(), lens.data_ptr(),
              _addr(held_lens), block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
              pairs.data_ptr(), lens_out.data_ptr(), held_lens_out.data_ptr(), free_count_out.data_ptr(), unserved.data_ptr())
@@ -1008,14 +1019,21 @@ def rglru_page_free(keep_lens: torch.Tensor, held_lens: torch.Tensor, block_tabl
     of at least rglru_page_free_workspace_bytes bytes, allocated here when None; calls sharing one must not overlap.
     Returns (held_lens_out [N], free_count_out [1])."""
     lib = _lib.load()
-    shape, dev = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
-    n = shape.n_seqs
-    _need(keep_lens, "keep_lens", (n,), torch.int32, dev)
-    held_lens_out, free_count_out = _pool_outs((held_lens_out, free_count_out), ("held_lens_out", "free_count_out"), (n, 1), dev)
-    workspace = _pool_scratch(workspace, int(lib.rglru_page_free_workspace_bytes(ctypes.byref(shape))), dev)
+    shape, dev, n, n_pages = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
+    i32 = torch.int32
+    _need(keep_lens, "keep_lens", (n,), i32, dev)
+    nbytes = _pool_bytes("rglru_page_free_workspace_bytes", n_pages, n, shape.max_pages, shape.page_size)
+    if _given((held_lens_out, free_count_out, workspace)):
+        held_lens_out = _out(held_lens_out, "held_lens_out", (n,), i32, dev)
+        free_count_out = _out(free_count_out, "free_count_out", (1,), i32, dev)
+        workspace = _pool_scratch(workspace, nbytes, dev)
+        nbytes = workspace.numel()
+    else:   # pieces of one allocation
+        workspace, held_lens_out, free_count_out = torch.empty(nbytes // 4 + n + 1, dtype=i32, device=dev).split_with_sizes(
+            (nbytes // 4, n, 1))
     _call_on(dev, lib.rglru_page_free, "rglru_page_free", ctypes.byref(shape), keep_lens.data_ptr(), held_lens.data_ptr(),
              block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-             held_lens_out.data_ptr(), free_count_out.data_ptr(), workspace.data_ptr(), workspace.numel())
+             held_lens_out.data_ptr(), free_count_out.data_ptr(), workspace.data_ptr(), nbytes)
     return held_lens_out, free_count_out
 
 
@@ -1034,21 +1052,31 @@ def rglru_page_compact(held_lens: torch.Tensor, block_table: torch.Tensor, share
     then -1; free_count_out [1]; pairs [min(keep_pages, n_pages - keep_pages), 2]: from, to, then -1; n_pairs [1];
     unmoved [1]: pages in use behind keep_pages that found no place)."""
     lib = _lib.load()
-    shape, dev = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
-    n_pages, keep = shape.n_pages, _int32("keep_pages", keep_pages)
+    shape, dev, n, n_pages = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
+    keep, width, i32 = _int32("keep_pages", keep_pages), shape.max_pages, torch.int32
     if keep > n_pages:
         raise ValueError(f"keep_pages is {keep}, expected at most {n_pages}")
     room = min(keep, n_pages - keep)
-    block_table_out = _out(block_table_out, "block_table_out", (shape.n_seqs, shape.max_pages), torch.int32, dev)
-    pairs = _out(pairs, "pairs", (room, 2), torch.int32, dev)
-    shares_out, free_pages_out, free_count_out, n_pairs, unmoved = _pool_outs(
-        (shares_out, free_pages_out, free_count_out, n_pairs, unmoved),
-        ("shares_out", "free_pages_out", "free_count_out", "n_pairs", "unmoved"), (n_pages, n_pages, 1, 1, 1), dev)
-    workspace = _pool_scratch(workspace, int(lib.rglru_page_compact_workspace_bytes(ctypes.byref(shape))), dev)
+    nbytes = _pool_bytes("rglru_page_compact_workspace_bytes", n_pages, n, width, shape.page_size)
+    if _given((block_table_out, shares_out, free_pages_out, free_count_out, pairs, n_pairs, unmoved, workspace)):
+        block_table_out = _out(block_table_out, "block_table_out", (n, width), i32, dev)
+        pairs = _out(pairs, "pairs", (room, 2), i32, dev)
+        shares_out = _out(shares_out, "shares_out", (n_pages,), i32, dev)
+        free_pages_out = _out(free_pages_out, "free_pages_out", (n_pages,), i32, dev)
+        free_count_out, n_pairs, unmoved = (_out(o, k, (1,), i32, dev) for o, k in (
+            (free_count_out, "free_count_out"), (n_pairs, "n_pairs"), (unmoved, "unmoved")))
+        workspace = _pool_scratch(workspace, nbytes, dev)
+        nbytes = workspace.numel()
+    else:   # pieces of two allocations: the workspace does not live on with the outputs
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        block_table_out, shares_out, free_pages_out, pairs, free_count_out, n_pairs, unmoved = torch.empty(
+            n * width + 2 * n_pages + 2 * room + 3, dtype=i32, device=dev).split_with_sizes(
+                (n * width, n_pages, n_pages, 2 * room, 1, 1, 1))
+        block_table_out, pairs = block_table_out.view(n, width), pairs.view(room, 2)
     _call_on(dev, lib.rglru_page_compact, "rglru_page_compact", ctypes.byref(shape), keep, held_lens.data_ptr(),
              block_table.data_ptr(), shares.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
              block_table_out.data_ptr(), shares_out.data_ptr(), free_pages_out.data_ptr(), free_count_out.data_ptr(),
-             pairs.data_ptr() if room else None, n_pairs.data_ptr(), unmoved.data_ptr(), workspace.data_ptr(), workspace.numel())
+             pairs.data_ptr() if room else None, n_pairs.data_ptr(), unmoved.data_ptr(), workspace.data_ptr(), nbytes)
     return block_table_out, shares_out, free_pages_out, free_count_out, pairs, n_pairs, unmoved
 
 
@@ -1065,21 +1093,24 @@ def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tens
     target of two pairs, or the source of one and the target of another."""
     lib = _lib.load()
     caches = list(caches)
-    if not caches or not all(isinstance(c, torch.Tensor) and c.dim() >= 1 and c.shape[0] > 0 for c in caches):
+    if not caches or not all(isinstance(c, torch.Tensor) and c.dim() > 0 for c in caches) or caches[0].shape[0] == 0:
         raise ValueError("caches must be tensors [n_pages, ...]")
     dev, n_pages = caches[0].device, caches[0].shape[0]
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
         raise ValueError("pairs must be a tensor [M, 2]")
-    m = _int32("the number of pairs", pairs.shape[0])
+    m = pairs.shape[0]
+    if (m | n_pages) >> 31:
+        raise ValueError(f"there are {m} pairs and {n_pages} pages, expected less than 2^31")
     _need(pairs, "pairs", (m, 2), torch.int32, dev)
     _opt(n_pairs, "n_pairs", (1,), torch.int32, dev)
-    sizes = []
+    sizes, at = [], []
     for c in caches:
         if c.device != dev or c.shape[0] != n_pages or not c.is_contiguous():
             raise ValueError(f"caches must be contiguous, on {dev}, with {n_pages} pages")
-        sizes.append(c.numel() // n_pages * c.element_size())
-    for i in range(0, len(caches), _lib.RGLRU_PAGE_COPY_ARRAYS):
-        part = caches[i: i + _lib.RGLRU_PAGE_COPY_ARRAYS]
-        arrays = (ctypes.c_void_p * len(part))(*[c.data_ptr() for c in part])
-        _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", _int32("n_pages", n_pages, 1), pairs.data_ptr() if m else None, m,
-                 _addr(n_pairs), len(part), arrays, _page_bytes(tuple(sizes[i: i + len(part)])))
+        sizes.append(c.nbytes // n_pages)
+        at.append(c.data_ptr())
+    most = _lib.RGLRU_PAGE_COPY_ARRAYS
+    for i in range(0, len(at), most):
+        part = at[i: i + most]
+        _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", n_pages, pairs.data_ptr() if m else None, m, _addr(n_pairs), len(part),
+                 (ctypes.c_void_p * len(part))(*part), _page_bytes(tuple(sizes[i: i + most])))
