@@ -60,8 +60,11 @@ rglru_status_t rglru_paged_kv_read_q4(const rglru_paged_shape_t* shape, const ui
  * they enter in three bf16 parts.
  *
  *   k_codes, k_scales, v_codes, v_scales : as above, each 16-byte aligned.
- *   workspace : rglru_paged_attn_q4_workspace_bytes(shape) bytes, 256-byte aligned;
- *               calls that share one must not overlap in time.
+ *   workspace : rglru_paged_attn_q4_workspace_bytes(shape) bytes, 256-byte aligned:
+ *               up to 203 MB whatever the lengths (what is used of it is a few MB in
+ *               a decode step), 40 bytes for every 128 rows of n_tokens * q_heads /
+ *               kv_heads (256 in bf16), 48 for every sequence and 8 for every key
+ *               head of one. Calls that share one must not overlap in time.
  * Everything else as for rglru_paged_attn_fwd. */
 size_t rglru_paged_attn_q4_workspace_bytes(const rglru_paged_shape_t* shape);
 rglru_status_t rglru_paged_attn_q4_fwd(const rglru_paged_shape_t* shape, const int32_t* cu_seqlens, const int32_t* kv_lens,

@@ -85,17 +85,8 @@ class Q4Batch:
                                            scale=scale, o=o, lse=lse, **kw)
 
     def check(self, o, lse, window=0, scale=None):
-        """Holds every row to the oracle.
-
-        Bound of a row that sees n keys, with A = sum p|v| per column and S the largest scale * sum |q||k|. Products of q
-        (float32: of its three bf16 parts, whose sizes add up to |q| (1 + 2^-7) at most) and a value of the cache are exact, each of the
-        c D sums (c = 1, float32 3) is off by at most 2^-24 of S: a score by e = (c D + 16) 2^-24 S, with scale, log2 e and the
-        argument of exp2; a weight relative to its sum by 2 e plus (c n + 16) 2^-23 (both sums, exp2, rescaling, merging,
-        division); bf16 adds half a step to every weight (2^-8 A; the block's power is exact) and to the result (2^-8 |o|),
-        float32 half a step to the result.
-        """
+        """Holds every row to the oracle (see hold)."""
         scale = self.dim ** -0.5 if scale is None else scale
-        half, c = HALF[self.dtype], 1 if self.dtype == torch.bfloat16 else 3
         o64, lse64 = o.cpu().double().numpy(), lse.cpu().double().numpy()
         assert (o64[self.tokens:] == 7.0).all() and (lse64[self.tokens:] == 7.0).all(), "padding rows were written"
         for i, m in enumerate(self.new):
@@ -104,21 +95,32 @@ class Q4Batch:
             rows = slice(int(self.cu[i]), int(self.cu[i + 1]))
             k, v = (paged_q4.values(oracle_paged.gather(self.cache[x], self.table[i], max(self.kv[i], 0)),
                                     oracle_paged.gather(self.cache[x + 1], self.table[i], max(self.kv[i], 0))) for x in (0, 2))
-            q = self.q[rows].double().numpy()
-            with np.errstate(invalid="ignore", over="ignore"):
-                ref, ref_lse, weight, size, seen = oracle_paged.attention(q, k, v, self.kv[i], window, scale)
-            fin = np.where(np.isfinite(size), size, 0.0)
-            e = (c * self.dim + 16) * 2.0 ** -24 * fin
-            rel = 2 * e + ((c * seen + 16) * 2.0 ** -23)[:, None]
-            tol = rel[..., None] * weight + half * np.abs(ref) * 1.01 + 1e-38
-            if self.dtype == torch.bfloat16:
-                tol += half * weight * 1.01
-            with np.errstate(invalid="ignore"):
-                err = np.abs(o64[rows] - ref)
-                same = (err <= tol) | (np.isnan(ref) & np.isnan(o64[rows])) | (ref == o64[rows])
-            assert same.all(), (i, np.argwhere(~same)[:5], o64[rows][~same][:5], ref[~same][:5], tol[~same][:5])
-            with np.errstate(invalid="ignore"):
-                err = np.abs(lse64[rows] - ref_lse)
-                ltol = e + ((c * seen + 16) * 2.0 ** -23)[:, None] + np.abs(ref_lse) * 2.0 ** -22
-                same = (err <= ltol) | (np.isnan(ref_lse) & np.isnan(lse64[rows])) | (ref_lse == lse64[rows])
-            assert same.all(), (i, "lse", np.argwhere(~same)[:5], lse64[rows][~same][:5], ref_lse[~same][:5])
+            hold(o64[rows], lse64[rows], self.q[rows].double().numpy(), k, v, self.kv[i], window, scale, self.dtype, i)
+
+
+def hold(o, lse, q, k, v, kv, window, scale, dtype, name=""):
+    """Holds the rows of one sequence, q [m, Hq, D] over k, v [Hkv, kv, D], to the oracle.
+
+    Bound of a row that sees n keys, with A = sum p|v| per column and S the largest scale * sum |q||k|. Products of q
+    (float32: of its three bf16 parts, whose sizes add up to |q| (1 + 2^-7) at most) and a value of the cache are exact, each of the
+    c D sums (c = 1, float32 3) is off by at most 2^-24 of S: a score by e = (c D + 16) 2^-24 S, with scale, log2 e and the
+    argument of exp2; a weight relative to its sum by 2 e plus (c n + 16) 2^-23 (both sums, exp2, rescaling, merging,
+    division); bf16 adds half a step to every weight (2^-8 A; the block's power is exact) and to the result (2^-8 |o|),
+    float32 half a step to the result.
+    """
+    half, c, dim = HALF[dtype], 1 if dtype == torch.bfloat16 else 3, q.shape[2]
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref, ref_lse, weight, size, seen = oracle_paged.attention(q, k, v, kv, window, scale)
+    fin = np.where(np.isfinite(size), size, 0.0)
+    e = (c * dim + 16) * 2.0 ** -24 * fin
+    rel = 2 * e + ((c * seen + 16) * 2.0 ** -23)[:, None]
+    tol = rel[..., None] * weight + half * np.abs(ref) * 1.01 + 1e-38
+    if dtype == torch.bfloat16:
+        tol += half * weight * 1.01
+    with np.errstate(invalid="ignore"):
+        same = (np.abs(o - ref) <= tol) | (np.isnan(ref) & np.isnan(o)) | (ref == o)
+    assert same.all(), (name, np.argwhere(~same)[:5], o[~same][:5], ref[~same][:5], tol[~same][:5])
+    with np.errstate(invalid="ignore"):
+        ltol = e + ((c * seen + 16) * 2.0 ** -23)[:, None] + np.abs(ref_lse) * 2.0 ** -22
+        same = (np.abs(lse - ref_lse) <= ltol) | (np.isnan(ref_lse) & np.isnan(lse)) | (ref_lse == lse)
+    assert same.all(), (name, "lse", np.argwhere(~same)[:5], lse[~same][:5], ref_lse[~same][:5])
