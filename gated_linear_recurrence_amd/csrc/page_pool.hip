@@ -242,7 +242,7 @@ __global__ __launch_bounds__(kThreads) void free_list_kernel(FreeArgs a) {
 // line, so that every thread has a few to look up beside each other. The first to give a page up marks it, further ones take
 // its count down; then every marked page either goes onto the list, its place from the sums over the marks, or has its count
 // taken down for the first one. A CU's atomics are slow (8 000 pages given up, 28 000 in the pool: 20 us with two on memory for each, 15 so).
-constexpr int kSmallFree = 1 << 14, kSmallCompact = 1 << 15, kSmallRows = 2048;   // entries of the table, rows
+constexpr int kSmallEntries = 1 << 15, kSmallRows = 2048;   // entries of the table, rows
 
 __global__ __launch_bounds__(kSmallThreads) void free_small_kernel(FreeArgs a) {
   __shared__ uint32_t gone[kSmallWords];
@@ -630,9 +630,10 @@ dim3 row_grid(const rglru_paged_shape_t& s) {
 }
 
 // Pools that one launch takes. us on the GPU, one launch and several: free, 8 000 entries of the table 10.4 and 9.0, 16 000 11.7
-// and 10.0, 32 000 15 and 11; compact 9.3 and 14.4, 11.1 and 15.2, 15 to 17 and 15 to 16. On the host every launch costs 2.6.
-bool small(const rglru_paged_shape_t& s, int entries) {
-  return s.n_pages <= kSmallPages && s.n_seqs <= kSmallRows && int64_t(s.n_seqs) * s.max_pages <= entries;
+// and 10.0, 32 000 15 and 11, 64 000 24 and 11; compact 9.3 and 14.4, 11.1 and 15.2, 15 to 17 and 15 to 16, 21 to 26 and 16. On
+// the host every launch costs 2.6, which decides where the GPU waits for it (free, 32 000 entries: 18 us a call with three).
+bool small(const rglru_paged_shape_t& s) {
+  return s.n_pages <= kSmallPages && s.n_seqs <= kSmallRows && int64_t(s.n_seqs) * s.max_pages <= kSmallEntries;
 }
 
 size_t free_bytes(const rglru_paged_shape_t& s) { return round_up(size_t(ceil_div(s.n_pages, kChunk)) * 4, 16); }
@@ -724,7 +725,7 @@ extern "C" rglru_status_t rglru_page_free(const rglru_paged_shape_t* sp, const i
   a.counts = static_cast<int32_t*>(workspace);
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (paged::small(s, paged::kSmallFree)) {
+  if (paged::small(s)) {
     paged::free_small_kernel<<<1, paged::kSmallThreads, 0, st>>>(a);
     return launch_status();
   }
@@ -781,7 +782,7 @@ extern "C" rglru_status_t rglru_page_compact(const rglru_paged_shape_t* sp, int6
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   a.most = int32_t(room);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (paged::small(s, paged::kSmallCompact)) {
+  if (paged::small(s)) {
     const int64_t all = paged::most(int64_t(s.n_seqs) * s.max_pages, s.n_pages);
     paged::compact_small_kernel<<<unsigned(ceil_div(all, paged::kSmallThreads)), paged::kSmallThreads, 0, st>>>(a);
     return launch_status();

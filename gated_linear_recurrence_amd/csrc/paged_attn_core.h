@@ -767,7 +767,8 @@ struct Wide {
   // What starting and ending a unit costs, in tiles: 15 us where a tile takes 1.6 (bf16, D = 256), 8 where it takes 1.9
   // (D = 128); float32 tiles take 16 times as long. At D = 64 126 calls (1 to 20 chunks of 100 to 2000 tokens after 0 to 4000,
   // with and without a window) take 0.6 % more in the mean with 3 and 0.7 % more with 8.
-  static constexpr int kOver = !kTiles16 ? 1 : D == 256 ? 9 : D == 128 ? 4 : 5;
+  // float32 on tiles of bf16: 3 (1 chunk of 2048 after 8000 137, 263, 468 us with 1 and 135, 265, 460 with 3 at D = 64, 128, 256).
+  static constexpr int kOver = !kTiles16 ? 1 : !kBf16 ? 3 : D == 256 ? 9 : D == 128 ? 4 : 5;
   static constexpr int kTileBytes = kKeys * D * int(sizeof(C));
 };
 
@@ -915,13 +916,12 @@ __device__ __forceinline__ void join_unit(const AttnArgs& a, const Cuts& cuts, i
 }
 
 template <typename E, int D, int kWideRows, bool kByUnit = false>
-__global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide_share, int narrow_share) {
+__global__ __launch_bounds__(kJoinThreads, kByUnit ? 3 : 5) void join_kernel(AttnArgs a, int wide_share, int narrow_share) {
   // workgroups: `wide_share` for each cut of the wide kernel, then `narrow_share` for each of the narrow one (kByUnit: each unit)
   const int wide_blocks = a.wide.grid * wide_share;
   const bool wide = int(blockIdx.x) < wide_blocks;
   const Cuts& cuts = wide ? a.wide : a.narrow;
-  const int64_t at = wide ? blockIdx.x : blockIdx.x - wide_blocks;
-  const int shares = wide ? wide_share : narrow_share;
+  const int at = wide ? blockIdx.x : blockIdx.x - wide_blocks, shares = wide ? wide_share : narrow_share;
   if (kByUnit && !wide) {
     // a unit that the narrow kernel has worked on has its entry
     for (int64_t i = at; i < int64_t(a.N) * a.Hkv * shares; i += gridDim.x - wide_blocks) {
@@ -941,11 +941,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(AttnArgs a, int wide
     }
     return;
   }
-  const int b = int(at) / shares, y = int(at) - b * shares;
+  const int b = at / shares, y = at - b * shares;
   const int pieces = cuts.joins[4 * b + 2];
   if (pieces == 0) return;
-  join_unit<E, D>(a, cuts, wide ? kWideRows : kNarrowRows, b, pieces, cuts.joins[4 * b], cuts.joins[4 * b + 1], cuts.joins[4 * b + 3],
-                  y, shares);
+  const int n = cuts.joins[4 * b], hk = cuts.joins[4 * b + 1], r0 = cuts.joins[4 * b + 3];
+  join_unit<E, D>(a, cuts, wide ? kWideRows : kNarrowRows, b, pieces, n, hk, r0, y, shares);
 }
 
 constexpr int kSlackPart = 32;  // a cut moves by up to this part of a stretch (an eighth of it to a 64th measured the same)

@@ -490,7 +490,7 @@ __global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kS
     total += sum;
   }
   if (total == 0) return;
-  const Line line(total, a.narrow.grid, kFewOver + 1);
+  const Line line(total, a.narrow.grid, 1);
   if (line.start(b0) >= total) return;
   int64_t found_before = 0;
   for (int n0 = 0;; n0 += P::kThreads) {

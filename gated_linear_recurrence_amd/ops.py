@@ -614,6 +614,7 @@ def _paged_attn_bytes(*fields) -> int:
 
 
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # 0.24 -> 0.1 us; a GPU tensor is there
 
 
 def _raw_stream(device) -> int:
@@ -627,7 +628,7 @@ def _call_on(device, fn, where, *args):
     """Calls a library function on the current stream of `device` (made current for it where another one is)."""
     if device.type != "cuda":
         raise ValueError(f"{where}: tensors are on {device}, expected a GPU")
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index is None or device.index == _current_device():
         status = fn(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -663,6 +664,10 @@ def _paged_cache(k_cache, v_cache, device):
 
 def _rows(t, name, heads, dim, dtype, device):
     """Checks packed rows [T, heads, dim], each row dense; returns (T, elements from one row to the next)."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.device == device and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim:
+            return shape[0], heads * dim
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if t.device != device:
@@ -947,13 +952,14 @@ def _pool(block_table, lens, name, shares, free_pages, free_count, page_size):
     n, width = block_table.shape
     if (n | width) >> 31:
         raise ValueError(f"block_table has shape {(n, width)}, expected less than 2^31 rows and columns")
-    _need(block_table, "block_table", (n, width), i32, dev)
-    _need(lens, name, (n,), i32, dev)
     if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
         raise ValueError("free_pages must be a tensor [n_pages]")
     n_pages = free_pages.shape[0]
-    _need(free_pages, "free_pages", (n_pages,), i32, dev)
-    _need(shares, "shares", (n_pages,), i32, dev)
+    rows, pages = (n,), (n_pages,)
+    _need(block_table, "block_table", (n, width), i32, dev)
+    _need(lens, name, rows, i32, dev)
+    _need(free_pages, "free_pages", pages, i32, dev)
+    _need(shares, "shares", pages, i32, dev)
     _need(free_count, "free_count", (1,), i32, dev)
     return _paged_shape(0, n_pages, n, width, _int32("page_size", page_size), 0, 0, 0, 0, 0, 0, 0.0, 0, 0), dev, n, n_pages
 
@@ -1093,7 +1099,7 @@ def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tens
     target of two pairs, or the source of one and the target of another."""
     lib = _lib.load()
     caches = list(caches)
-    if not caches or not all(isinstance(c, torch.Tensor) and c.dim() > 0 for c in caches) or caches[0].shape[0] == 0:
+    if not caches or not isinstance(caches[0], torch.Tensor) or caches[0].dim() == 0 or caches[0].shape[0] == 0:
         raise ValueError("caches must be tensors [n_pages, ...]")
     dev, n_pages = caches[0].device, caches[0].shape[0]
     if not isinstance(pairs, torch.Tensor) or pairs.dim() != 2 or pairs.shape[1] != 2:
@@ -1105,7 +1111,7 @@ def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tens
     _opt(n_pairs, "n_pairs", (1,), torch.int32, dev)
     sizes, at = [], []
     for c in caches:
-        if c.device != dev or c.shape[0] != n_pages or not c.is_contiguous():
+        if not isinstance(c, torch.Tensor) or c.device != dev or c.shape[:1] != (n_pages,) or not c.is_contiguous():
             raise ValueError(f"caches must be contiguous, on {dev}, with {n_pages} pages")
         sizes.append(c.nbytes // n_pages)
         at.append(c.data_ptr())
