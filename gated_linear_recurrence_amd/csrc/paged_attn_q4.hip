@@ -186,8 +186,9 @@ __device__ __forceinline__ float quarter_sum(float x) {
   return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// A wave's bound on the scales of its values: from kSpan below it on up to itself they pass as weights' exponents.
-constexpr int kSpan = 100;
+// A wave's bound on the scales of its values: from kSpan below it on up to itself they pass as weights' exponents. A weight of
+// 2^-80 then still enters as a normal bf16, whatever a key that the row does not see adds to the bound.
+constexpr int kSpan = 30;
 
 // Whether a key's scales (byte by byte) lie within the span.
 template <int kP>

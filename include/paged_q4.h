@@ -57,7 +57,8 @@ rglru_status_t rglru_paged_kv_read_q4(const rglru_paged_shape_t* shape, const ui
  * the values as they are and q as it is (float32 queries in three bf16 parts,
  * which hold all of their bits), in float32. For bf16 the softmax weights are
  * rounded to bf16 where they enter the product with the values; for float32
- * they enter in three bf16 parts.
+ * they enter in three bf16 parts. Weights of 2^-80 of a row's largest and less
+ * may count as nothing, beside a NaN too.
  *
  *   k_codes, k_scales, v_codes, v_scales : as above, each 16-byte aligned.
  *   workspace : rglru_paged_attn_q4_workspace_bytes(shape) bytes, 256-byte aligned:

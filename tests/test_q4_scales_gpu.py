@@ -56,14 +56,16 @@ def test_columns_of_their_own_size(gpu_lib, dtype, dim, case):
 @pytest.mark.parametrize("window", [0, 60])
 @pytest.mark.parametrize("case", range(3))
 def test_what_is_not_seen_is_huge(gpu_lib, dtype, dim, window, case):
-    """The largest scale there is, or NaN, in keys that a row does not see (behind the window, later tokens of a chunk) leaves no trace."""
+    """Larger scales, the largest there is, or NaN, in keys that a row does not see (behind the window, later tokens of a chunk): no bit
+    of it changes."""
     c = CASES[case]
-    b, plain = batch(c, dim, dtype, dim + case), batch(c, dim, dtype, dim + case)
+    b = plain = batch(c, dim, dtype, dim + case)
     want = run(gpu_lib, plain, window=window)
     first = [b.kv[i] - c["new"][i] for i in range(2)]   # the position of a sequence's first row
     hidden = lambda i, j: j > first[i] or (window > 0 and j <= first[i] - window)  # noqa: E731
-    for big in (252, 255):
-        rescale(b, lambda i, j, s: np.full_like(s, big) if hidden(i, j) else s)
+    for big in (lambda s: s + 25, lambda s: s + 40, lambda s: s + 95, lambda s: 0 * s + 252, lambda s: 0 * s + 255, lambda s: 0 * s + 1):
+        b = batch(c, dim, dtype, dim + case)
+        rescale(b, lambda i, j, s: big(s) if hidden(i, j) else s)  # noqa: B023
         o, lse = b.call(gpu_lib, window=window)
         for i in range(2):
             row = int(b.cu[i])
