@@ -484,21 +484,27 @@ __device__ __forceinline__ int32_t select(const uint32_t* bits, const int32_t* b
 __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArgs a) {
   __shared__ uint32_t go[kSmallWords], to[kSmallWords];   // pages to move, places
   __shared__ int32_t go_before[kSmallWords], to_before[kSmallWords];
+  __shared__ int32_t have[kSmallRows];   // pages of a row
   __shared__ int32_t part[kSmallThreads / 64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, words = (a.r.n_pages + 31) / 32;
+  const int tid = threadIdx.x, words = (a.r.n_pages + 31) / 32, entries = a.r.N * a.r.width;
   for (int w = tid; w < words; w += kSmallThreads) go[w] = to[w] = 0;
+  for (int n = tid; n < a.r.N; n += kSmallThreads) have[n] = pages_of(a.r, a.held[n]);
   __syncthreads();
   const int32_t listed = min(max(a.count[0], 0), a.r.n_pages);
   for (int i = tid; i < listed; i += kSmallThreads) {
     const int32_t p = a.free_pages[i];
     if (p >= 0 && p < a.r.n_pages) atomicOr(to + p / 32, 1u << (p % 32));
   }
-  for (int n = wave; n < a.r.N; n += kSmallThreads / 64) {
-    const int32_t have = pages_of(a.r, a.held[n]);
-    const int32_t* const row = a.r.table + int64_t(n) * a.r.width;
-    for (int32_t j = lane; j < have; j += 64) {
-      const int32_t p = row[j];
-      if (p >= 0 && p < a.r.n_pages) atomicOr(go + p / 32, 1u << (p % 32));
+  constexpr int kAhead = 4;
+  for (int i0 = tid; i0 < entries; i0 += kAhead * kSmallThreads) {
+    int32_t page[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) page[k] = a.r.table[min(i0 + k * kSmallThreads, entries - 1)];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * kSmallThreads, n = i / a.r.width;
+      if (i < entries && i - n * a.r.width < have[n] && page[k] >= 0 && page[k] < a.r.n_pages)
+        atomicOr(go + page[k] / 32, 1u << (page[k] % 32));
     }
   }
   __syncthreads();
@@ -526,10 +532,10 @@ __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArg
     return before[p / 32] + __popc(bits[p / 32] & ((1u << (p % 32)) - 1));
   };
   auto marked = [](const uint32_t* bits, int32_t p) { return bits[p / 32] >> (p % 32) & 1; };
-  for (int i = start; i < a.r.N * a.r.width; i += threads) {
+  for (int i = start; i < entries; i += threads) {
     const int n = i / a.r.width;
     int32_t p = a.r.table[i];
-    if (p >= a.keep && p < a.r.n_pages && i - n * a.r.width < pages_of(a.r, a.held[n])) {   // so it is marked
+    if (p >= a.keep && p < a.r.n_pages && i - n * a.r.width < have[n]) {   // so it is marked
       const int32_t rank = rank_of(go, go_before, p);
       if (rank < moves) p = select(to, to_before, words, rank);
     }
@@ -629,9 +635,10 @@ dim3 row_grid(const rglru_paged_shape_t& s) {
   return dim3(unsigned(x), unsigned(least(ceil_div(s.max_pages, kSlice), most(2048 / x, 1))));
 }
 
-// Pools that one launch takes. us on the GPU, one launch and several: free, 8 000 entries of the table 10.4 and 9.0, 16 000 11.7
-// and 10.0, 32 000 15 and 11, 64 000 24 and 11; compact 9.3 and 14.4, 11.1 and 15.2, 15 to 17 and 15 to 16, 21 to 26 and 16. On
-// the host every launch costs 2.6, which decides where the GPU waits for it (free, 32 000 entries: 18 us a call with three).
+// Pools that one launch takes. us on the GPU, one launch and several: free, 8 000 entries of the table 10.3 and 9.1, 16 000 11.6
+// and 9.9, 32 000 15 and 11.9, 64 000 24 and 12; compact 9.1 and 14.7, 11.8 and 15.4, 17 and 15 to 16, 26 and 17 (8.8 and 14.6
+// for 6 000 entries in 192 rows). On the host every launch costs 2.6, which decides where the GPU waits for it (free, 32 000
+// entries: 18 us a call with three).
 bool small(const rglru_paged_shape_t& s) {
   return s.n_pages <= kSmallPages && s.n_seqs <= kSmallRows && int64_t(s.n_seqs) * s.max_pages <= kSmallEntries;
 }
