@@ -76,6 +76,8 @@ __device__ __forceinline__ int32_t pages_of(const Rows& r, int32_t tokens) {
 // One launch: a page is popped at most once a row, so a row's place in the list
 // is the number of rows before it that ask for one, which every workgroup counts
 // for itself (16 bytes a row, from L2) before it serves its own rows, one per wave.
+// 5.5 us for 64 answers to 8 questions of up to 2000 tokens in pages of 16, 6.2 for 256
+// rows of 512.
 struct ForkArgs {
   Rows r;
   const int32_t* from;
@@ -171,7 +173,8 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs a) {
 // Three launches: every row takes its pages' counts down (a page that nobody
 // holds any more ends below 0, however often it was given up); chunks of the
 // pool count those; and each chunk, which then knows how many lie in the chunks
-// after it, writes its own to the list and sets their counts back to 0.
+// after it, writes its own to the list and sets their counts back to 0. 1024 rows of
+// up to 8192 tokens in pages of 16, 254 000 pages: 13 us.
 constexpr int kEach = 8, kChunk = kThreads * kEach;  // pages of a thread and of a workgroup
 constexpr int kSlice = 1024;                         // columns of a row that a wave works on
 
@@ -572,7 +575,9 @@ __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArg
 // ---- copy ----
 //
 // Bound by HBM: a workgroup copies pieces of up to kPieceBytes of one page of one
-// array, 16 bytes a thread and load, all loads of a piece before its stores.
+// array, 16 bytes a thread and load, all loads of a piece before its stores. 96 MB
+// of pages of 34 KB: 32 us (5.9 TB/s of reads and writes; 40 where the caches were
+// not touched before).
 constexpr int kLoads = 4, kPieceBytes = kThreads * 16 * kLoads;
 
 struct CopyArgs {

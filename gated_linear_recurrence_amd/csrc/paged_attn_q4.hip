@@ -8,7 +8,12 @@
 // differs: each wave fetches its share of the codes into registers while the tile
 // before is worked on, and writes the values, which bf16 holds exactly, once for
 // all waves. float32 queries and weights enter as three bf16 parts, 3 products of
-// bf16 where float32 ones take 16 times as long.
+// bf16 where float32 ones take 16 times as long. 2048 tokens after 30 011, 32 and
+// 8 heads of 128: 0.98 to 1.02 ms by card (1.02 to 1.07 PFLOP/s; over a bf16 cache
+// 0.91 to 1.00); float32, 2048 after 8000, 8 and 4 heads of 64 / 128 / 256: 134 /
+// 263 / 458 us (307 / 667 / 1250 over a float32 cache with float32 products).
+// The values' writes have 2-way bank conflicts, a sixth of the LDS cycles; without
+// them the time was the same.
 //
 // Few rows (decode steps, drafts): see below.
 #include <hip/hip_runtime.h>
@@ -83,26 +88,31 @@ struct Staged {
 
 // ---- few rows: at most 32 per unit (decode steps, drafts) ----
 //
-// Bound by the bytes of the cache and close behind by the vector units, which
-// turn codes into values: a key and a value of 128 elements cost 136 bytes and,
-// at 16 rows, some 8 vector instructions of a wave. A wave therefore holds 16 rows
-// (two sets of them where there are more) as the columns of S^T = K Q^T in 16x16
-// products, and streams tiles of 64 keys of its own through LDS as they lie in
-// memory, codes and scales.
+// Bound by the bytes of the cache and next by the vector units, which turn codes
+// into values: a key and a value of 128 elements cost 136 bytes and, at 16 rows,
+// 7 vector instructions of a wave. A wave therefore holds 16 rows (two sets of
+// them where there are more) as the columns of S^T = K Q^T in 16x16 products, and
+// streams tiles of 64 keys of its own through LDS as they lie in memory, codes and
+// scales. 64 decodes over up to 16k tokens, 32 and 8 heads of 128: 113 us and a
+// join of 6 (5.1 TB/s; 5.6 over 260k tokens a sequence, 48 of the 113 us would be
+// vector instructions alone). float32, 32 drafts over up to 4k tokens, 16 heads of
+// 64: 30 us, of them 8 of start and end (3.8 TB/s at length: three weights to
+// lower and three products where bf16 has one).
 //
 // S^T: lane (m, g) = (lane % 16, lane / 16) reads a quarter of row m of 16 keys,
 // elements (D / 4) g on, and turns it into operands; the sum over the elements
 // does not care for their order, so the queries are held in the same one. A block
-// of keys lies within a lane's quarter (or two quarters within a block), so the power is an
-// operand of the conversion.
+// of keys lies within a lane's quarter (or two quarters within a block), so the
+// power is an operand of the conversion.
 //
 // O^T = V^T P^T: the accumulator of S^T (keys 4g .. 4g + 3 of every 16, row m) is
 // the operand of P^T up to the order of the keys. The transposing 4-bit LDS read
 // hands a lane 16 keys of one column, in rows of the lane's own choice: 16 j + 4g + i.
-// Their powers differ within a pair that the conversion takes, so V enters as codes and the powers go
-// into the weights, a set of weights per block of columns: exact, and a value that is
-// not finite stays out of the products of rows that do not see it, as codes are
-// always finite.
+// Their powers differ within a pair that the conversion takes, so V enters as codes
+// and the powers go into the weights, a set of weights per block of columns: exact,
+// and a value that is not finite stays out of the products of rows that do not see
+// it, as codes are always finite. Scales of a tile that lie further apart than
+// the weights' exponents allow are taken in bands, a pass over the values each.
 constexpr int kFewKeys = 64, kFewOver = 1;
 
 template <typename E>
