@@ -1023,7 +1023,8 @@ def rglru_page_free(keep_lens: torch.Tensor, held_lens: torch.Tensor, block_tabl
     shares [n_pages] and free_pages [n_pages] are updated in place: a page that other rows hold stays theirs, one
     that nobody holds any more goes onto the stack, those of a call in descending order. workspace: a uint8 device tensor
     of at least rglru_page_free_workspace_bytes bytes, allocated here when None; calls sharing one must not overlap.
-    Returns (held_lens_out [N], free_count_out [1])."""
+    A row that goes back to inside a page that other rows hold keeps it shared and may not write there: go back to a
+    page's end, or fork the row anew. Returns (held_lens_out [N], free_count_out [1])."""
     lib = _lib.load()
     shape, dev, n, n_pages = _pool(block_table, held_lens, "held_lens", shares, free_pages, free_count, page_size)
     i32 = torch.int32
@@ -1116,7 +1117,9 @@ def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tens
         sizes.append(c.nbytes // n_pages)
         at.append(c.data_ptr())
     most = _lib.RGLRU_PAGE_COPY_ARRAYS
-    for i in range(0, len(at), most):
-        part = at[i: i + most]
-        _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", n_pages, pairs.data_ptr() if m else None, m, _addr(n_pairs), len(part),
-                 (ctypes.c_void_p * len(part))(*part), _page_bytes(tuple(sizes[i: i + most])))
+    # more caches than a call takes: without pairs first, so that nothing is copied if one of them is refused
+    for pairs_of in ((0, m) if len(at) > most else (m,)):
+        for i in range(0, len(at), most):
+            part = at[i: i + most]
+            _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", n_pages, pairs.data_ptr() if pairs_of else None, pairs_of,
+                     _addr(n_pairs), len(part), (ctypes.c_void_p * len(part))(*part), _page_bytes(tuple(sizes[i: i + most])))

@@ -60,6 +60,9 @@ rglru_status_t rglru_page_fork(const rglru_paged_shape_t* shape, const int32_t* 
  * rows hold stays with them (shares - 1 for every row that gives it up); one that
  * nobody holds any more goes onto the free list: those of one call in descending
  * order, so that the first page of the pool among them comes off first.
+ * A row that goes back to inside a page that other rows hold (fewer tokens than were
+ * shared, and not a multiple of page_size) keeps it shared: it may be read and
+ * forked from, but no new token of it may be written.
  *
  *   keep_lens     : [N] int32; held_lens or more keeps all, 0 ends the request.
  *   held_lens     : [N] int32.

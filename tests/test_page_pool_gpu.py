@@ -105,6 +105,33 @@ def test_copy_of_many_caches_and_none(gpu_lib):
     assert all(torch.equal(x, y) for x, y in zip(caches, want))
 
 
+def test_nothing_is_copied_where_a_cache_is_refused(gpu_lib):
+    """The last of more caches than one launch takes is not aligned: the call raises and leaves all of them."""
+    caches = [torch.randn(6, 64, device="cuda") for _ in range(70)]
+    want = [c.clone() for c in caches]
+    odd = torch.zeros(6 * 64 + 1, device="cuda")[1:].view(6, 64)
+    with pytest.raises(RuntimeError, match="align"):
+        gpu_lib.rglru_page_copy(i32([[5, 0]]), caches + [odd])
+    assert all(torch.equal(x, y) for x, y in zip(caches, want)) and not bool(odd.any())
+
+
+def test_rows_that_go_back_share_to_the_end_of_a_page(gpu_lib):
+    """Two rows share a prompt; both go back to a page's end and go on: fresh pages for the new tokens, the others stay shared."""
+    page, width, n_pages = 16, 8, 20
+    table = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+    table[0, :5] = i32([3, 4, 5, 6, 7])
+    shares, free = torch.zeros(n_pages, dtype=torch.int32, device="cuda"), i32(list(range(19, 7, -1)) + [0] * 8)
+    _, lens, held, count, unserved = gpu_lib.rglru_page_fork(i32([-1, 0]), i32([80, 0]), table, shares, free, i32([12]), page_size=page)
+    assert lens.tolist() == [80, 80] and int(unserved) == 0 and shares[3:8].tolist() == [1] * 5
+    held, count = gpu_lib.rglru_page_free(i32([48, 32]), held, table, shares, free, count, page_size=page)
+    assert held.tolist() == [48, 32] and shares[3:8].tolist() == [1, 1, 0, 0, 0] and int(count) == 14
+    slots, _, kv, held, count, unserved = gpu_lib.rglru_page_plan(held, i32([0, 3, 6]), table, free, count, n_tokens=6, page_size=page,
+                                                                  held_lens=held)
+    assert int(unserved) == 0 and kv.tolist() == [51, 35]
+    at = (slots // page).tolist()
+    assert len(set(at)) == 2 and not set(at) & {3, 4, 5} and table[:, :3].tolist() == [[3, 4, 5], [3, 4, at[3]]]
+
+
 def test_copy_past_32_bit_offsets(gpu_lib):
     cache = torch.zeros(70, 1 << 26, dtype=torch.uint8, device="cuda")
     cache[69].fill_(3)
