@@ -170,6 +170,10 @@ struct Narrow4 {
   static constexpr int kWaves = 4, kThreads = kWaves * 64, kStretches = kWaves;
   // Workgroups on a CU, as many as the registers allow without spills.
   static constexpr int kGroups = D == 256 || (D == 128 && kSets == 2 && sizeof(E) == 4) ? 1 : D == 64 && kSets == 1 ? 3 : 2;
+  // Two sets of float32 queries of 256 elements take 192 registers, which spills 469 of them; with their third parts in LDS 186,
+  // of which 29 are read again in a tile (32 x 32 rows over 4000 tokens, 4 key heads: 175 -> 121 us).
+  static constexpr bool kRest = D == 256 && kSets == 2 && sizeof(E) == 4;
+  static constexpr int kRestBytes = kRest ? kSets * (D / 32) * 1024 : 0;   // of a wave
   // Pages of 8 keys each, looked up two tiles ahead.
   static constexpr int kSegs = kFewKeys / kSeg, kRing = 2, kPageBytes = kRing * kSegs * 4;
   __device__ static constexpr int swz(int r) {
@@ -221,6 +225,7 @@ struct Wave4 {
   O q[kSets][D / 32];
   f32x4 o[kSets][D / 16];
   float m[kSets], c[kSets], l[kSets];   // as in Wave
+  lds_u8* rest;   // this lane's third parts, 1024 bytes apart
   int32_t lo[kSets], hi[kSets];
 
   // This lane's share of the queries of its rows, elements (D / 4) g on, as they lie in memory ..
@@ -255,6 +260,7 @@ struct Wave4 {
         if constexpr (sizeof(E) == 2) q[z][x].w = raw.w[z][x];
         else q[z][x] = split_query(raw.w[z][2 * x], raw.w[z][2 * x + 1]);
         if (a.q_sign <= 0) set_bits(q[z][x], keep, flip);
+        if constexpr (P::kRest) *(lds_u32x4*)(rest + (z * (D / 32) + x) * 1024) = q[z][x].w[2];
       }
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) o[z][x] = 0.0f;
@@ -263,6 +269,12 @@ struct Wave4 {
       hi[z] = r < rows ? max(s.kv - s.fresh + r / a.group, -1) : -1;
       lo[z] = a.window > 0 ? max(hi[z] - a.window + 1, 0) : 0;
     }
+  }
+
+  __device__ __forceinline__ O query(int z, int x) const {
+    O f = q[z][x];
+    if constexpr (P::kRest) f.w[2] = *(const lds_u32x4*)(rest + (z * (D / 32) + x) * 1024);
+    return f;
   }
 
   // A lane's share of keys 16 j + lane % 16: codes and powers.
@@ -311,7 +323,7 @@ struct Wave4 {
       for (int x = 0; x < D / 32; ++x) {
         const u32x4 k = values_of(now.w[x], now.power[x / 4]);
 #pragma unroll
-        for (int z = 0; z < kSets; ++z) s[z][j] = mma16(k, q[z][x], s[z][j]);
+        for (int z = 0; z < kSets; ++z) s[z][j] = mma16(k, query(z, x), s[z][j]);
       }
       order();
     }
@@ -532,7 +544,9 @@ __global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kS
   int64_t rest = uniform(found_rest[wave]);   // position within the sequence's units
   Seq s = {__builtin_amdgcn_readfirstlane(found[wave].start), __builtin_amdgcn_readfirstlane(found[wave].fresh),
            __builtin_amdgcn_readfirstlane(found[wave].kv)};
+  __shared__ __align__(16) unsigned char rest_buf[P::kWaves * P::kRestBytes + 16];
   W w;
+  w.rest = (lds_u8*)rest_buf + wave * P::kRestBytes + lane * 16;
   lds_u8* const mine = (lds_u8*)buf + wave * P::kTileBytes;
   const uint32_t mine_at = uint32_t(uintptr_t(mine));
   lds_u8* const ring = (lds_u8*)page_buf + wave * P::kPageBytes;
@@ -746,6 +760,9 @@ __global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kS
 template <typename E, int D>
 constexpr int kFewUnits4 = sizeof(E) == 4 || D == 64 ? 64 : 40;
 
+// One set of rows where no unit has more than 16, else two: 32 x 16 rows over 4000 tokens, 4 key heads of 64 / 128 / 256, take
+// 26 / 31 / 44 us with one and 28 / 34 / 54 with two in bf16, 30 / 37 / 56 and 36 / 49 / 163 in float32. 32 x 32 rows take 29 /
+// 39 / 57 us with two and 62 / 75 / 122 in the wide kernel, 38 / 53 / 121 and 65 / 130 / 207 in float32.
 template <typename E, int D>
 Plan plan4_of(const rglru_paged_shape_t& s) {
   using W = Wide<E, D, uint16_t>;
