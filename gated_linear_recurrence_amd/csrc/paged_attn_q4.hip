@@ -111,8 +111,8 @@ struct Staged {
 // Their powers differ within a pair that the conversion takes, so V enters as codes
 // and the powers go into the weights, a set of weights per block of columns: exact,
 // and a value that is not finite stays out of the products of rows that do not see
-// it, as codes are always finite. Scales of a tile that lie further apart than
-// the weights' exponents allow are taken in bands, a pass over the values each.
+// it, as codes are always finite. Scales of a tile that lie in different bands
+// (see Band) are taken a band at a time, a pass over the values each.
 constexpr int kFewKeys = 64, kFewOver = 1;
 
 template <typename E>
@@ -200,13 +200,30 @@ __device__ __forceinline__ float quarter_sum(float x) {
   return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// A wave's bound on the scales of its values: from kSpan below it on up to itself they pass as weights' exponents. A weight of
-// 2^-80 then still enters as a normal bf16, whatever a key that the row does not see adds to the bound.
-constexpr int kSpan = 30;
+// Scales of values pass as weights' exponents, lowered from the top of a scale's band. The bands' borders are fixed, so what
+// becomes of a key, and which keys are summed in one pass, depends on its own scale alone; borders drawn from a tile's largest scale
+// would let a key that a row does not see change that row's rounding. Widths: a weight of 2^-80 is still a normal bf16 46 steps
+// lower; the third part of a float32 one starts 2^-16 below it. The usual band is 104 to 149 in bf16 (blocks whose largest value is
+// 7e-7 to 2e7) and 112 to 142 in float32 (2e-4 to 2e5). Tiles whose values lie across a border take a pass for each band: 64 x 1
+// after 7999, 16 / 4 heads of 64 / 128 / 256, take 39 / 56 / 112 us in bf16 and 60 / 88 / 206 with two bands in every tile, 48 / 70 /
+// 145 and 75 / 113 / 256 in float32.
+template <typename E>
+struct Band {
+  static constexpr int kWidth = sizeof(E) == 2 ? 46 : 31, kFirst = sizeof(E) == 2 ? 11 : 18;   // kFirst: the lowest top
+  static constexpr int kUsual = kFirst + (sizeof(E) == 2 ? 3 : 4) * kWidth;
+  static constexpr int kLast = kFirst + (252 - kFirst) / kWidth * kWidth;   // the highest top below 252, which ends the last one
+  // 253 and 254 stand alone: values with them may pass bf16.
+  __device__ static constexpr int top(int e) {
+    return e > 252 ? e : e > kLast ? 252 : e <= kFirst ? kFirst : (e - kFirst + kWidth - 1) / kWidth * kWidth + kFirst;
+  }
+  __device__ static constexpr int low(int top) {
+    return top > 252 ? top : top > kLast ? kLast + 1 : top <= kFirst ? 0 : top - kWidth + 1;
+  }
+};
 
-// Whether a key's scales (byte by byte) lie within the span.
+// Whether a key's scales (byte by byte) lie between `low` and `ref`.
 template <int kP>
-__device__ __forceinline__ bool within(const uint32_t* w, int ref) {
+__device__ __forceinline__ bool within(const uint32_t* w, int ref, int low) {
   const u16x2 top = {uint16_t(ref), uint16_t(ref)};
   u16x2 far = 0;
 #pragma unroll
@@ -214,7 +231,7 @@ __device__ __forceinline__ bool within(const uint32_t* w, int ref) {
     far = __builtin_elementwise_max(far, top - __builtin_bit_cast(u16x2, w[i] & 0x00FF00FFu));
     far = __builtin_elementwise_max(far, top - __builtin_bit_cast(u16x2, w[i] >> 8 & 0x00FF00FFu));
   }
-  return max(far[0], far[1]) <= kSpan;
+  return max(far[0], far[1]) <= ref - low;
 }
 
 // kSets sets of 16 rows of one wave.
@@ -413,8 +430,8 @@ struct Wave4 {
   }
 
   // Adds 64 weighted values to the output: the values as their codes times 2^(ref - 127), the weights (bf16, none negative)
-  // times 2^(e - ref), subtracted from their exponents down to 0. For scales e from ref - kSpan to ref; a weight beside a scale of
-  // 255 counts as 0.
+  // times 2^(e - ref), subtracted from their exponents down to 0. For scales e of the band below ref; a weight beside a scale of 255
+  // counts as 0.
   __device__ __forceinline__ void values(const lds_u8* codes, const lds_u8* scales, int ref, int lane, const O (*p)[2]) {
     const Scales sc = scales_of(scales, lane);
     int at = rows_at(lane);
@@ -462,9 +479,7 @@ struct Wave4 {
         }
         hit |= uint32_t(__shfl_xor(int(hit), 16));
         hit |= uint32_t(__shfl_xor(int(hit), 32));
-        const float add = hit != 0 ? __uint_as_float(0x7FC00000u) : 0.0f;
-        o[z][2 * b] += add;
-        o[z][2 * b + 1] += add;
+        if (hit != 0) o[z][2 * b] = o[z][2 * b + 1] = __uint_as_float(0x7FC00000u);
         order();
       }
   }
@@ -631,7 +646,7 @@ __global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kS
     load_keys();
     load_values();
     w.start(before, s, raw, rows, lane);
-    int ref = 0;
+    int ref = Band<E>::kUsual, low = Band<E>::low(ref);
     for (int32_t t = t0; t < t1; ++t) {
       const bool next = t + 1 < t1;
       const int32_t kv0 = (x.lo + t) * kFewKeys;
@@ -675,23 +690,30 @@ __global__ __launch_bounds__((Narrow4<E, D, kSets>::kThreads), (Narrow4<E, D, kS
         for (int d = 32; d > 0; d /= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
         return int(__builtin_amdgcn_readfirstlane(top));
       };
-      bool bands = __any(there && !within<P::kP>(own, ref));
+      auto next_band = [&]() {
+        ref = Band<E>::top(largest());
+        low = Band<E>::low(ref);
+      };
+      bool bands = __any(there && !within<P::kP>(own, ref, low));
       if (bands) {
-        ref = largest();
-        bands = __any(there && !within<P::kP>(own, ref));
-        if (bands) w.mark(scales + P::kScaleBytes, lane, p);
+        next_band();
+        bands = __any(there && !within<P::kP>(own, ref, low));
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < kBytes; ++i) odd |= uint32_t(byte(i) == 255u);
+        if (__any(there && odd)) w.mark(scales + P::kScaleBytes, lane, p);
       }
       for (;;) {
         bool more = false;
         if (bands) {
-          // scales too far apart, or NaN: a band of them at a time, 255 for the others
-          ref = largest();
+          // more than one band, or NaN: a band at a time, 255 for the others
+          next_band();
           uint32_t now[kBytes / 4] = {}, left = 0;
 #pragma unroll
           for (int i = 0; i < kBytes; ++i) {
-            const bool in = int(byte(i)) <= ref && int(byte(i)) >= ref - kSpan;
+            const bool in = int(byte(i)) <= ref && int(byte(i)) >= low;
             now[i / 4] |= (in ? byte(i) : 255u) << (8 * (i % 4));
-            left |= uint32_t(!in && int(byte(i)) < ref);
+            left |= uint32_t(!in && int(byte(i)) < low);
             if (in) own[i / 4] |= 255u << (8 * (i % 4));
           }
           more = __any(there && left);
