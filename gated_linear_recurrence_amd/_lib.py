@@ -34,6 +34,7 @@ class rglru_shape_t(ctypes.Structure):
     ]
 
 
+RGLRU_ERR_INVALID_ARGUMENT = 1
 RGLRU_PAGE_COPY_ARRAYS = 64
 RGLRU_DELTA_GDN = 0
 RGLRU_DELTA_KDA = 1

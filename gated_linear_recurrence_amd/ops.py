@@ -1117,9 +1117,23 @@ def rglru_page_copy(pairs: torch.Tensor, caches, *, n_pairs: Optional[torch.Tens
         sizes.append(c.nbytes // n_pages)
         at.append(c.data_ptr())
     most = _lib.RGLRU_PAGE_COPY_ARRAYS
-    # more caches than a call takes: without pairs first, so that nothing is copied if one of them is refused
-    for pairs_of in ((0, m) if len(at) > most else (m,)):
-        for i in range(0, len(at), most):
-            part = at[i: i + most]
-            _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", n_pages, pairs.data_ptr() if pairs_of else None, pairs_of,
-                     _addr(n_pairs), len(part), (ctypes.c_void_p * len(part))(*part), _page_bytes(tuple(sizes[i: i + most])))
+    groups = [(at[i: i + most], _page_bytes(tuple(sizes[i: i + most]))) for i in range(0, len(at), most)]
+
+    def call(part, page_bytes, count):
+        _call_on(dev, lib.rglru_page_copy, "rglru_page_copy", n_pages, pairs.data_ptr() if m else None, count, _addr(n_pairs),
+                 len(part), (ctypes.c_void_p * len(part))(*part), page_bytes)
+
+    if len(groups) > 1:   # nothing is copied if any of them is refused
+        for part, page_bytes in groups:
+            call(part, page_bytes, 0)
+        _check_apart(at, [n_pages * s for s in sizes], [(pairs.data_ptr(), 8 * m), (_addr(n_pairs) or 0, 4)], "rglru_page_copy")
+    for part, page_bytes in groups:
+        call(part, page_bytes, m)
+
+
+def _check_apart(at, sizes, inputs, where):
+    """Refuses arrays, by address and size, that overlap each other or an input, as the library does within one call."""
+    order = sorted(zip(at, sizes))
+    near = any(a + size > b for (a, size), (b, _) in zip(order, order[1:]))
+    if near or any(a < x + n and x < a + size for x, n in inputs if x and n for a, size in order):
+        _lib.check(_lib.RGLRU_ERR_INVALID_ARGUMENT, where)
