@@ -889,10 +889,7 @@ def rglru_paged_kv_read_q4(k_codes: torch.Tensor, k_scales: torch.Tensor, v_code
         raise ValueError("slot_map must be a tensor [T]")
     t = slot_map.numel()
     _need(slot_map, "slot_map", (t,), torch.int32, dev)
-    if k is None and v is None:
-        k, v = torch.empty((2, t, heads, dim), dtype=dtype, device=dev).unbind()
-    else:
-        k, v = _out(k, "k", (t, heads, dim), dtype, dev), _out(v, "v", (t, heads, dim), dtype, dev)
+    k, v = _out(k, "k", (t, heads, dim), dtype, dev), _out(v, "v", (t, heads, dim), dtype, dev)
     shape = _paged_shape(t, n_pages, 0, 0, page_size, 0, heads, dim, _IO[dtype], 0, 0, 0.0, 0, 0)
     _call_on(dev, lib.rglru_paged_kv_read_q4, "rglru_paged_kv_read_q4", ctypes.byref(shape), k_codes.data_ptr(),
              k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr(), slot_map.data_ptr(), k.data_ptr(), v.data_ptr())
