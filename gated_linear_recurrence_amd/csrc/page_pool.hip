@@ -52,8 +52,8 @@ __device__ __forceinline__ int32_t block_sum(int32_t v, int32_t* part) {
   return total;
 }
 
-// A bit for every page, in LDS: pools of up to kSmallPages pages.
-constexpr int kSmallThreads = 1024, kSmallPages = 1 << 17, kSmallWords = kSmallPages / 32;
+// The kernels that hold a bit for every page in LDS (see small_free and small_compact).
+constexpr int kSmallThreads = 1024;
 
 // The pages of a word from `first` on.
 __device__ __forceinline__ uint32_t bits_from(int word, int32_t first) {
@@ -245,29 +245,26 @@ __global__ __launch_bounds__(kThreads) void free_list_kernel(FreeArgs a) {
 // line, so that every thread has a few to look up beside each other. The first to give a page up marks it, further ones take
 // its count down; then every marked page either goes onto the list, its place from the sums over the marks, or has its count
 // taken down for the first one. A CU's atomics are slow (8 000 pages given up, 28 000 in the pool: 20 us with two on memory for each, 15 so).
-constexpr int kSmallEntries = 1 << 15, kSmallRows = 2048;   // entries of the table, rows
+constexpr int kFreePages = 1 << 13, kFreeRows = 64, kFreeEntries = 1 << 14;   // of the pool, of the table
+constexpr int kFreeWords = kFreePages / 32;
+static_assert(kFreeWords <= kSmallThreads && kFreeRows <= kSmallThreads, "a thread sums up one word, one row");
 
 __global__ __launch_bounds__(kSmallThreads) void free_small_kernel(FreeArgs a) {
-  __shared__ uint32_t gone[kSmallWords];
-  __shared__ int32_t before[kSmallWords];
-  __shared__ int32_t stays[kSmallRows], ends[kSmallRows];   // a row's first entry given up; entries of the rows up to it
+  __shared__ uint32_t gone[kFreeWords];
+  __shared__ int32_t before[kFreeWords];
+  __shared__ int32_t stays[kFreeRows], ends[kFreeRows];   // a row's first entry given up; entries of the rows up to it
   __shared__ int32_t part[kSmallThreads / 64];
   const int tid = threadIdx.x, lane = tid & 63, words = (a.r.n_pages + 31) / 32, padded = (a.r.n_pages + 63) / 64 * 64;
   for (int w = tid; w < padded / 32; w += kSmallThreads) gone[w] = 0;
-  int32_t all = 0;
-  for (int n0 = 0; n0 < a.r.N; n0 += kSmallThreads) {
-    const int n = n0 + tid;
-    int32_t given = 0, total;
-    if (n < a.r.N) {
-      const int32_t held = a.held[n], kept = min(max(a.keep[n], 0), held);
-      a.held_out[n] = kept;
-      stays[n] = pages_of(a.r, kept);
-      given = max(pages_of(a.r, held) - stays[n], 0);
-    }
-    const int32_t upto = block_inclusive<kSmallThreads>(given, part, total);
-    if (n < a.r.N) ends[n] = all + upto;
-    all += total;
+  int32_t given = 0, all;
+  if (tid < a.r.N) {
+    const int32_t held = a.held[tid], kept = min(max(a.keep[tid], 0), held);
+    a.held_out[tid] = kept;
+    stays[tid] = pages_of(a.r, kept);
+    given = max(pages_of(a.r, held) - stays[tid], 0);
   }
+  const int32_t through = block_inclusive<kSmallThreads>(given, part, all);
+  if (tid < a.r.N) ends[tid] = through;
   __syncthreads();
   constexpr int kAhead = 4;
   for (int i0 = tid; i0 < all; i0 += kAhead * kSmallThreads) {
@@ -309,14 +306,9 @@ __global__ __launch_bounds__(kSmallThreads) void free_small_kernel(FreeArgs a) {
     }
   }
   __syncthreads();
-  const int each = (words + kSmallThreads - 1) / kSmallThreads, first = tid * each, end = min(first + each, words);
-  int32_t mine = 0, total;
-  for (int w = first; w < end; ++w) mine += __popc(gone[w]);
-  int32_t upto = block_inclusive<kSmallThreads>(mine, part, total) - mine;
-  for (int w = first; w < end; ++w) {
-    before[w] = upto;
-    upto += __popc(gone[w]);
-  }
+  int32_t total;
+  const int32_t mine = tid < words ? __popc(gone[tid]) : 0, upto = block_inclusive<kSmallThreads>(mine, part, total);
+  if (tid < words) before[tid] = upto - mine;
   __syncthreads();
   const int32_t count = min(max(a.count[0], 0), a.r.n_pages);
   for (int p = tid; p < a.r.n_pages; p += kSmallThreads) {
@@ -484,10 +476,14 @@ __device__ __forceinline__ int32_t select(const uint32_t* bits, const int32_t* b
   return lo * 32 + __ffs(left) - 1;
 }
 
+constexpr int kCompactPages = 1 << 15, kCompactRows = 2048, kCompactEntries = 1 << 15;   // of the pool, of the table
+constexpr int kCompactWords = kCompactPages / 32;
+static_assert(kCompactWords <= kSmallThreads, "a thread sums up one word");
+
 __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArgs a) {
-  __shared__ uint32_t go[kSmallWords], to[kSmallWords];   // pages to move, places
-  __shared__ int32_t go_before[kSmallWords], to_before[kSmallWords];
-  __shared__ int32_t have[kSmallRows];   // pages of a row
+  __shared__ uint32_t go[kCompactWords], to[kCompactWords];   // pages to move, places
+  __shared__ int32_t go_before[kCompactWords], to_before[kCompactWords];
+  __shared__ int32_t have[kCompactRows];   // pages of a row
   __shared__ int32_t part[kSmallThreads / 64];
   const int tid = threadIdx.x, words = (a.r.n_pages + 31) / 32, entries = a.r.N * a.r.width;
   for (int w = tid; w < words; w += kSmallThreads) go[w] = to[w] = 0;
@@ -511,22 +507,19 @@ __global__ __launch_bounds__(kSmallThreads) void compact_small_kernel(CompactArg
     }
   }
   __syncthreads();
-  const int each = (words + kSmallThreads - 1) / kSmallThreads, first = tid * each, end = min(first + each, words);
   int32_t go_mine = 0, to_mine = 0, go_all, to_all;
-  for (int w = first; w < end; ++w) {
-    const uint32_t behind = bits_from(w, a.keep), used = go[w];
-    to[w] &= ~used & ~behind;
-    go[w] = used & behind;
-    go_mine += __popc(go[w]);
-    to_mine += __popc(to[w]);
+  if (tid < words) {
+    const uint32_t behind = bits_from(tid, a.keep), used = go[tid];
+    to[tid] &= ~used & ~behind;
+    go[tid] = used & behind;
+    go_mine = __popc(go[tid]);
+    to_mine = __popc(to[tid]);
   }
-  int32_t go_at = block_inclusive<kSmallThreads>(go_mine, part, go_all) - go_mine;
-  int32_t to_at = block_inclusive<kSmallThreads>(to_mine, part, to_all) - to_mine;
-  for (int w = first; w < end; ++w) {
-    go_before[w] = go_at;
-    to_before[w] = to_at;
-    go_at += __popc(go[w]);
-    to_at += __popc(to[w]);
+  const int32_t go_upto = block_inclusive<kSmallThreads>(go_mine, part, go_all);
+  const int32_t to_upto = block_inclusive<kSmallThreads>(to_mine, part, to_all);
+  if (tid < words) {
+    go_before[tid] = go_upto - go_mine;
+    to_before[tid] = to_upto - to_mine;
   }
   __syncthreads();
   const int32_t moves = min(go_all, to_all), left = to_all - moves;
@@ -640,13 +633,25 @@ dim3 row_grid(const rglru_paged_shape_t& s) {
   return dim3(unsigned(x), unsigned(least(ceil_div(s.max_pages, kSlice), most(2048 / x, 1))));
 }
 
-// Pools that one launch takes. us on the GPU, one launch and several: free, 8 000 entries of the table 10.3 and 9.1, 16 000 11.6
-// and 9.9, 32 000 15 and 11.9, 64 000 24 and 12; compact 9.1 and 14.7, 11.8 and 15.4, 17 and 15 to 16, 26 and 17 (8.8 and 14.6
-// for 6 000 entries in 192 rows). On the host every launch costs 2.6, which decides where the GPU waits for it (free, 32 000
-// entries: 18 us a call with three).
-bool small(const rglru_paged_shape_t& s) {
-  return s.n_pages <= kSmallPages && s.n_seqs <= kSmallRows && int64_t(s.n_seqs) * s.max_pages <= kSmallEntries;
+// Pools that one launch takes: every launch costs the host 2.6 us, but one workgroup (free) or each one (compact) passes over all
+// bits of the pool. us on the GPU (replayed from a graph) and of a call among others, one launch and several:
+//            rows, entries, pages     GPU               call
+//   free     64, 1000, 600            6.9 and 7.6       10.4 and 15.5
+//            64, 16 000, 8000         11.3 and 9.9      11.2 and 15.4
+//            128, 16 000, 8000        11.9 and 9.1      11.9 and 15.1
+//            64, 32 000, 16 000       16.4 and 11.7     16.3 and 15.2
+//            64, 1000, 131 000        44 and 8.8        44 and 15
+//   compact  64, 1000, 600            5.7 and 12.8      14.9 and 24.4
+//            64, 32 000, 32 000       16.8 and 15.8     17.1 and 25.4
+//            2000, 32 000, 32 000     17.4 and 14.7     17.8 and 25.3
+//            64, 1000, 61 000         16.5 and 14.7     16.7 and 24
+//            64, 1000, 131 000        28 and 15.5       29 and 24
+// The bounds are where one launch starts to lose more than a fifth on the GPU; up to there a call costs 4 to 10 us less.
+bool small(const rglru_paged_shape_t& s, int64_t pages, int rows, int64_t entries) {
+  return s.n_pages <= pages && s.n_seqs <= rows && int64_t(s.n_seqs) * s.max_pages <= entries;
 }
+bool small_free(const rglru_paged_shape_t& s) { return small(s, kFreePages, kFreeRows, kFreeEntries); }
+bool small_compact(const rglru_paged_shape_t& s) { return small(s, kCompactPages, kCompactRows, kCompactEntries); }
 
 size_t free_bytes(const rglru_paged_shape_t& s) { return round_up(size_t(ceil_div(s.n_pages, kChunk)) * 4, 16); }
 
@@ -737,7 +742,7 @@ extern "C" rglru_status_t rglru_page_free(const rglru_paged_shape_t* sp, const i
   a.counts = static_cast<int32_t*>(workspace);
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (paged::small(s)) {
+  if (paged::small_free(s)) {
     paged::free_small_kernel<<<1, paged::kSmallThreads, 0, st>>>(a);
     return launch_status();
   }
@@ -794,7 +799,7 @@ extern "C" rglru_status_t rglru_page_compact(const rglru_paged_shape_t* sp, int6
   a.chunks = int32_t(ceil_div(s.n_pages, paged::kChunk));
   a.most = int32_t(room);
   const hipStream_t st = static_cast<hipStream_t>(stream);
-  if (paged::small(s)) {
+  if (paged::small_compact(s)) {
     const int64_t all = paged::most(int64_t(s.n_seqs) * s.max_pages, s.n_pages);
     paged::compact_small_kernel<<<unsigned(ceil_div(all, paged::kSmallThreads)), paged::kSmallThreads, 0, st>>>(a);
     return launch_status();

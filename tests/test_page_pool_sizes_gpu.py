@@ -18,32 +18,40 @@ def same(got, want):
     np.testing.assert_array_equal(got.cpu().numpy().reshape(-1), np.asarray(want).reshape(-1))
 
 
-# rows, tokens a page, most tokens, spare pages, columns (None: those of the longest row)
+# rows, tokens a page, most tokens, spare pages, pages of the pool before those (None: as many as the rows hold) or columns of the table
 SIZES = {
     "long rows": (24, 8, 16000, 50, None),                    # slices past the first, several launches
     "very long rows": (5, 8, 80000, 3, None),
-    "33 000 free pages": (9, 8, 100, 33000, None),            # one launch, more than a word of marks a thread
-    "2^17 pages": (40, 8, 400, 0, "up to 2^17"),              # the last pool of one launch
-    "2^17 + 1 pages": (40, 8, 400, 1, "up to 2^17"),          # the first of several
+    "2^13 pages": (40, 8, 400, 0, 1 << 13),                   # the last pool of one launch of free
+    "2^13 + 1 pages": (40, 8, 400, 1, 1 << 13),
+    "2^15 pages": (40, 8, 400, 0, 1 << 15),                   # the last pool of one launch of compact
+    "2^15 + 1 pages": (40, 8, 400, 1, 1 << 15),
+    "2^14 entries": (16, 8, 4000, 20, "1024 columns"),        # as many as one launch of free takes
+    "more than 2^14 entries": (16, 8, 4000, 20, "1025 columns"),
+    "2^15 entries": (32, 8, 6000, 20, "1024 columns"),        # as many as one launch of compact takes
+    "more than 2^15 entries": (32, 8, 6000, 20, "1025 columns"),
+    "33 000 free pages": (9, 8, 100, 33000, None),
+    "2^17 pages": (40, 8, 400, 0, 1 << 17),
+    "2^17 + 1 pages": (40, 8, 400, 1, 1 << 17),
     "530 000 pages": (30, 8, 4000, 530000, None),             # more than 256 chunks
-    "2^15 entries": (32, 8, 6000, 20, 1024),
-    "more than 2^15 entries": (32, 8, 6000, 20, 1025),
-    "2048 rows": (2048, 8, 60, 5, None),
-    "2049 rows": (2049, 8, 60, 5, None),
+    "64 rows": (64, 8, 600, 5, None),                         # the most rows of one launch of free
+    "65 rows": (65, 8, 600, 5, None),
+    "2048 rows": (2048, 8, 50, 5, None),                      # of compact
+    "2049 rows": (2049, 8, 50, 5, None),
 }
 
 
 def pool_of(name, rng):
-    n, page, most, spare, width = SIZES[name]
-    if width == "up to 2^17":
-        s = random_pool(np.random.default_rng(n), n=n, page=page, most=most, spare=0)
-        more = (1 << 17) + spare - len(s["free"])
+    n, page, most, spare, size = SIZES[name]
+    if isinstance(size, int):
+        s = random_pool(rng, n=n, page=page, most=most, spare=0)
+        more = size + spare - len(s["free"])
         extra = len(s["free"]) + rng.permutation(more)
         s["shares"] = np.concatenate([s["shares"], np.zeros(more, np.int32)])
         s["free"] = np.concatenate([s["free"][: s["count"]], extra, np.full(len(s["free"]) - s["count"], -7)]).astype(np.int32)
         s["count"] += more
         return s, page, most
-    return random_pool(rng, n=n, page=page, most=most, spare=spare, width=width), page, most
+    return random_pool(rng, n=n, page=page, most=most, spare=spare, width=size and int(size.split()[0])), page, most
 
 
 @pytest.mark.parametrize("name", SIZES)
