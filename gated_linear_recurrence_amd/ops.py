@@ -990,7 +990,8 @@ def rglru_page_fork(fork_from: torch.Tensor, lens: torch.Tensor, block_table: to
     were taken for. block_table [N, max_pages] and shares [n_pages] (the rows that hold a page beyond the first) are
     updated in place: full pages are shared, a last one that is not full gets a page from the stack free_pages, to be
     filled by rglru_page_copy(pairs, caches). A row whose source is itself, forked in this call or not there, that is
-    not empty, or for which no page is left is not served and stays as it was.
+    not empty, or for which no page is left is not served and stays as it was. States of recurrent layers, a row each,
+    go along by rglru_page_copy with pairs (fork_from[n], n) for the rows with lens_out > lens and -1, -1 for the others.
     Returns (pairs [N, 2]: from, to or -1, -1; lens_out [N]; held_lens_out [N]; free_count_out [1]; unserved [1])."""
     lib = _lib.load()
     shape, dev, n, _ = _pool(block_table, lens, "lens", shares, free_pages, free_count, page_size)

@@ -38,6 +38,10 @@ extern "C" {
  * holds nothing (lens and held_lens 0) and, where it needs a page, the
  * list still has one after all rows before it asked; any other is left as it was
  * and counted in unserved. Rows with fork_from < 0 are left as they were.
+ * What belongs to a row and not to its pages, the state of a recurrent layer, is the
+ * caller's to take along, for the rows whose lens_out is more than lens: with pairs
+ * (fork_from[n], n) for those and -1, -1 for the others, rglru_page_copy does it over
+ * the states of all layers (n_pages = N, a row a page).
  *
  *   fork_from     : [N] int32.
  *   lens          : [N] int32, tokens of every row (those that a fork takes over).
