@@ -25,9 +25,9 @@
 // infinite value is NaN. The values of a tile that some row does not see in
 // full are therefore looked at first; where one is not finite, products of 0/1
 // operands mark the (row, column) pairs that see a +inf, a -inf or a NaN, and
+// those values are replaced by 0 in LDS before the tile is worked on.
 #pragma once
 
-// those values are replaced by 0 in LDS before the tile is worked on.
 #include <hip/hip_runtime.h>
 
 #include "paged_common.h"

@@ -168,10 +168,11 @@ struct Narrow4 {
   static constexpr int kTileBytes = 2 * kCodes + 2 * kScaleBytes;
   static constexpr int kLoadRows = 64 / kP;   // rows that one load of codes fetches
   static constexpr int kWaves = 4, kThreads = kWaves * 64, kStretches = kWaves;
-  // Workgroups on a CU, as many as the registers allow without spills (none more than one at D = 256).
+  // Workgroups on a CU: as many as the registers of float32 allow without spills, one at D = 256. One set of bf16 (124 registers at
+  // D = 64, 160 at 128) would fit another one, which was not timed.
   static constexpr int kGroups = D == 256 || (D == 128 && kSets == 2 && sizeof(E) == 4) ? 1 : D == 64 && kSets == 1 ? 3 : 2;
-  // Two sets of float32 queries of 256 elements take 192 registers, which spills 469 of them; with their third parts in LDS 186,
-  // of which 29 are read again in a tile (32 x 32 rows over 4000 tokens, 4 key heads: 175 -> 121 us).
+  // Two sets of float32 queries of 256 elements take 192 registers, which spills 469 of them; with their third parts in LDS 178
+  // (32 x 32 rows over 4000 tokens, 4 key heads: 175 -> 116 us).
   static constexpr bool kRest = D == 256 && kSets == 2 && sizeof(E) == 4;
   static constexpr int kRestBytes = kRest ? kSets * (D / 32) * 1024 : 0;   // of a wave
   // Pages of 8 keys each, looked up two tiles ahead.

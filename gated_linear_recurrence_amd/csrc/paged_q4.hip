@@ -1,8 +1,8 @@
 // Write and read-back of the 4-bit paged cache (include/paged_q4.h).
 //
 // Both are bound by HBM: a block of 32 elements costs 64 bytes of bf16 and 17
-// of the cache. 14 500 tokens of 8 heads of 128 in bf16, keys and values: the write
-// 15.4 to 16.7 us, the read-back 16.1 to 16.5 (4.6 to 4.9 TB/s). A thread holds 8 elements of a row (16 bytes of bf16), four
+// of the cache. 16 200 tokens of 8 heads of 128, keys and values: in bf16 the write 15.2 to 16.7 us, the read-back 16.1 to 16.5 (4.5
+// to 4.9 TB/s), in float32 23.8 and 26.9 (5.9 and 5.3 TB/s). A thread holds 8 elements of a row (16 bytes of bf16), four
 // neighbours a block: its largest magnitude takes two DPP steps on the bits
 // (as integers, so that infinities and NaN stay the largest), its power a few
 // integer operations, its codes one conversion instruction for two elements:

@@ -123,7 +123,8 @@ rglru_status_t rglru_paged_kv_write(const rglru_paged_shape_t* shape, const void
  * A row that sees no key (p < 0, or all its scores -inf) gets o = 0 and lse =
  * -inf; one with a score of +inf or NaN gets NaN in both. What a row does not
  * see has no influence on it, infinities and NaN included (at given lengths
- * not on a bit of it); padding rows of o and lse are left as they were.
+ * not on a bit of it, the sign of a zero apart); padding rows of o and lse are
+ * left as they were.
  * Weights of 2^-118 of a row's largest and less, the 0 of a score of -inf
  * among them, may count as nothing: a finite value adds nothing there, an
  * infinite one gives infinity or NaN. Sums are formed with weights up to 2^8
